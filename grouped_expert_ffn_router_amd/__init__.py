@@ -17,6 +17,9 @@ Functions carry the C names:
     moe_payload_bytes     the dispatch + combine closed form 2 * k * H * bytes * tokens
     moe_grouped_ffn_train     moe_grouped_ffn keeping h and the gate/up pre-activations (training)
     moe_grouped_ffn_backward  dout -> dx, expert weight gradients, routing-weight and logit gradients
+    moe_norm                  x [T, H] (+ residual)           -> Norm(y [T, H] (+ fp8 scales), sum, mean, rstd)
+    moe_norm_backward         dy, rows, mean, rstd            -> dx, dweight, dbias
+    moe_orthogonalize         g [B, m, n]                     -> orthogonalised update [B, m, n]
 
 ``MoELayer`` chains the four calls with preallocated buffers for repeated use.
 
@@ -48,7 +51,11 @@ EXPORTS = [
     "moe_grouped_ffn_gate_up_gather", "moe_grouped_ffn_down_scatter", "moe_grouped_ffn_fused", "moe_combine_slots",
     "moe_dispatch_permute_capacity", "moe_router_topk", "moe_grouped_ffn_train",
     "moe_grouped_ffn_backward_workspace_bytes", "moe_grouped_ffn_backward", "moe_dispatch_permute_noalloc",
+    "moe_norm", "moe_norm_backward_workspace_bytes", "moe_norm_backward", "moe_orthogonalize_workspace_bytes",
+    "moe_orthogonalize",
 ]
+MOE_NORM_LAYER, MOE_NORM_RMS = 0, 1
+NORM_KINDS = {"layer": MOE_NORM_LAYER, "rms": MOE_NORM_RMS}
 
 
 class FfnWeights(ctypes.Structure):
@@ -64,6 +71,7 @@ def _load():
         raise ImportError(f"{LIB_PATH} is missing: build it with __graft_entry__.build() (hipcc, gfx950)")
     L = ctypes.CDLL(LIB_PATH)
     P, i64, i32, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
+    f32 = ctypes.c_float
     st = ctypes.c_int
     sig = {
         "moe_status_string": (ctypes.c_char_p, [st]),
@@ -92,6 +100,11 @@ def _load():
                                        P]),
         "moe_combine_slots": (st, [P, P, P, i64, i32, i32, i32, i32, P, st, P]),
         "moe_dispatch_permute_capacity": (st, [P, P, st, i64, i32, P, i32, i32, i32, P, P, P, P, P, P, P, sz, P]),
+        "moe_norm": (st, [P, i64, P, i64, st, i64, i32, st, P, P, st, f32, P, P, P, st, P, P, P]),
+        "moe_norm_backward_workspace_bytes": (sz, [i64, i32]),
+        "moe_norm_backward": (st, [P, i64, P, i64, P, i64, st, i64, i32, st, P, st, P, P, P, P, P, P, sz, P]),
+        "moe_orthogonalize_workspace_bytes": (sz, [i64, i32, i32, st]),
+        "moe_orthogonalize": (st, [P, st, i64, i32, i32, i32, f32, f32, f32, f32, f32, P, st, P, sz, P]),
         "moe_dispatch_permute_noalloc": (st, [P, P, st, i64, i32, P, i32, i32, P, P, P, P, P, P, P]),
     }
     for name, (res, args) in sig.items():
@@ -444,6 +457,221 @@ def moe_combine_slots(y_slot, topk_idx, e_lo=0, E_local=None, out_dtype=torch.bf
     return out
 
 
+def _on_device(fn, dev, stream):
+    """Context of a call on tensors of device ``dev``: kernels are launched with that device current."""
+    if dev.type != "cuda":
+        raise ValueError(f"{fn}: tensors must be on the GPU (got {dev})")
+    if isinstance(stream, torch.cuda.Stream) and stream.device != dev:
+        raise ValueError(f"{fn}: the stream is on {stream.device}, the tensors on {dev}")
+    return contextlib.nullcontext() if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+
+
+def _tensor(fn, name, t, shape, dtypes, dev, contiguous=True):
+    """Checks one tensor argument against what the C call assumes of its pointer; returns it."""
+    if t.shape != shape:
+        raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{fn}: {name} has dtype {t.dtype}, not {' or '.join(map(str, dtypes))}")
+    if t.device != dev:
+        raise ValueError(f"{fn}: {name} is on {t.device}, not {dev}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{fn}: {name} must be contiguous")
+    return t
+
+
+def _rows(fn, name, t, shape, dtype, dev):
+    """Checks rows whose values are contiguous and whose stride is free; returns the stride in elements."""
+    _tensor(fn, name, t, shape, (dtype,), dev, contiguous=False)
+    T, H = shape
+    if H > 1 and t.stride(1) != 1:
+        raise ValueError(f"{fn}: {name}'s rows must be contiguous")
+    if T <= 1:
+        return H
+    if t.stride(0) < H:
+        raise ValueError(f"{fn}: {name}'s rows overlap")
+    return t.stride(0)
+
+
+_ROW_TYPES = (torch.float32, torch.bfloat16)
+_FP8_TYPES = (torch.uint8, torch.float8_e4m3fn)
+
+
+@dataclasses.dataclass
+class Norm:
+    y: torch.Tensor
+    y_scales: torch.Tensor | None
+    sum: torch.Tensor  # the rows that were normalised: x + residual, or x itself
+    mean: torch.Tensor | None
+    rstd: torch.Tensor
+
+
+def _norm_args(fn, x, weight, kind):
+    if kind not in NORM_KINDS:
+        raise ValueError(f"{fn}: kind {kind!r} is not one of {tuple(NORM_KINDS)}")
+    if x.dim() != 2:
+        raise ValueError(f"{fn}: rows must be [T, H] (got {tuple(x.shape)})")
+    if x.dtype not in _ROW_TYPES:
+        raise ValueError(f"{fn}: rows must be float32 or bfloat16 (got {x.dtype})")
+    _tensor(fn, "weight", weight, (x.shape[1],), _ROW_TYPES, x.device)
+    return x.shape
+
+
+def moe_norm(x, weight, bias=None, residual=None, kind="layer", eps=1e-5, out_dtype=None, y=None, y_scales=None,
+             sum=None, mean=None, rstd=None, stream=None) -> Norm:
+    """Layer norm (kind "layer") or RMS norm ("rms") of the rows x, or of x + residual (stored in ``sum``).
+
+    x, residual: [T, H] float32 or bfloat16, rows of any stride.  weight, bias: [H] float32 or bfloat16 (both alike).
+    out_dtype: x's (default), or torch.float8_e4m3fn / torch.uint8: e4m3 codes with y_scales [T, H/128], as
+    moe_dispatch_permute takes them.  ``sum`` may be x or residual themselves."""
+    fn = "moe_norm"
+    T, H = _norm_args(fn, x, weight, kind)
+    dev = x.device
+    ldx = _rows(fn, "x", x, (T, H), x.dtype, dev)
+    ldr = 0 if residual is None else _rows(fn, "residual", residual, (T, H), x.dtype, dev)
+    if bias is not None:
+        _tensor(fn, "bias", bias, (H,), (weight.dtype,), dev)
+    if y is not None and out_dtype is not None and y.dtype != out_dtype:
+        raise ValueError(f"{fn}: y has dtype {y.dtype}, not {out_dtype}")
+    yt = y.dtype if y is not None else out_dtype or x.dtype
+    fp8 = yt in _FP8_TYPES
+    if not fp8 and yt != x.dtype:
+        raise NotImplementedError(f"{fn}: the output is the rows' dtype or e4m3 codes, not {yt}")
+    if fp8 and H % 128:
+        raise ValueError(f"{fn}: e4m3 rows need H = {H} to be a multiple of 128")
+    layer = kind == "layer"
+    with _on_device(fn, dev, stream):
+        if (y is None or rstd is None or (fp8 and y_scales is None) or (layer and mean is None)
+                or (residual is not None and sum is None)):
+            with _alloc_on(stream):
+                if y is None:
+                    y = torch.empty((T, H), dtype=yt, device=dev)
+                if fp8 and y_scales is None:
+                    y_scales = torch.empty((T, H // 128), dtype=torch.float32, device=dev)
+                if residual is not None and sum is None:
+                    sum = torch.empty((T, H), dtype=x.dtype, device=dev)
+                if layer and mean is None:
+                    mean = torch.empty(T, dtype=torch.float32, device=dev)
+                if rstd is None:
+                    rstd = torch.empty(T, dtype=torch.float32, device=dev)
+        _tensor(fn, "y", y, (T, H), (yt,), dev)
+        _tensor(fn, "rstd", rstd, (T,), (torch.float32,), dev)
+        if fp8:
+            _tensor(fn, "y_scales", y_scales, (T, H // 128), (torch.float32,), dev)
+        if layer:
+            _tensor(fn, "mean", mean, (T,), (torch.float32,), dev)
+        if residual is not None:
+            _tensor(fn, "sum", sum, (T, H), (x.dtype,), dev)
+        _check(lib.moe_norm(_ptr(x), ldx, _ptr(residual), ldr, dtype_code(x.dtype), T, H, NORM_KINDS[kind],
+                            _ptr(weight), _ptr(bias), dtype_code(weight.dtype), eps,
+                            _ptr(sum) if residual is not None else None, _ptr(y), _ptr(y_scales) if fp8 else None,
+                            dtype_code(yt), _ptr(mean) if layer else None, _ptr(rstd), _stream(stream)), fn)
+    return Norm(y, y_scales if fp8 else None, sum if residual is not None else x, mean if layer else None, rstd)
+
+
+def moe_norm_backward_workspace_bytes(T, H) -> int:
+    return lib.moe_norm_backward_workspace_bytes(T, H)
+
+
+def moe_norm_backward(dy, rows, weight, mean, rstd, kind="layer", dsum=None, want_bias=None, out=None, workspace=None,
+                      stream=None):
+    """Gradients of moe_norm for dy = dL/dy: dict(dx [T, H], dweight [H] fp32, dbias [H] fp32 or None).
+
+    rows: what was normalised (Norm.sum); dx is its gradient, with dsum (the gradient that reaches the rows by the
+    residual stream) added.  dx may be dy or dsum themselves (out["dx"]).  want_bias: default, for kind "layer" only."""
+    fn = "moe_norm_backward"
+    T, H = _norm_args(fn, rows, weight, kind)
+    dev, dt = rows.device, rows.dtype
+    layer = kind == "layer"
+    if want_bias is None:
+        want_bias = layer if out is None else out.get("dbias") is not None
+    ld_s = _rows(fn, "rows", rows, (T, H), dt, dev)
+    ld_dy = _rows(fn, "dy", dy, (T, H), dt, dev)
+    ld_ds = 0 if dsum is None else _rows(fn, "dsum", dsum, (T, H), dt, dev)
+    if layer:
+        if mean is None:
+            raise ValueError(f"{fn}: kind 'layer' needs the rows' means")
+        _tensor(fn, "mean", mean, (T,), (torch.float32,), dev)
+    _tensor(fn, "rstd", rstd, (T,), (torch.float32,), dev)
+    with _on_device(fn, dev, stream):
+        if out is None or workspace is None:
+            with _alloc_on(stream):
+                if out is None:
+                    out = dict(dx=torch.empty((T, H), dtype=dt, device=dev),
+                               dweight=torch.empty(H, dtype=torch.float32, device=dev),
+                               dbias=torch.empty(H, dtype=torch.float32, device=dev) if want_bias else None)
+                if workspace is None:
+                    workspace = torch.empty(moe_norm_backward_workspace_bytes(T, H), dtype=torch.uint8, device=dev)
+        _tensor(fn, "dx", out["dx"], (T, H), (dt,), dev)
+        _tensor(fn, "dweight", out["dweight"], (H,), (torch.float32,), dev)
+        if want_bias:
+            if out.get("dbias") is None:
+                raise ValueError(f"{fn}: want_bias needs out['dbias']")
+            _tensor(fn, "dbias", out["dbias"], (H,), (torch.float32,), dev)
+        _workspace(fn, workspace, dev)
+        _check(lib.moe_norm_backward(_ptr(dy), ld_dy, _ptr(rows), ld_s, _ptr(dsum), ld_ds, dtype_code(dt), T, H,
+                                     NORM_KINDS[kind], _ptr(weight), dtype_code(weight.dtype),
+                                     _ptr(mean) if layer else None, _ptr(rstd), _ptr(out["dx"]), _ptr(out["dweight"]),
+                                     _ptr(out["dbias"]) if want_bias else None, _ptr(workspace), _nbytes(workspace),
+                                     _stream(stream)), fn)
+    return out
+
+
+def _nbytes(t) -> int:
+    return t.numel() * t.element_size()
+
+
+def _workspace(fn, t, dev):
+    if t.device != dev or not t.is_contiguous():
+        raise ValueError(f"{fn}: the workspace must be contiguous and on {dev}")
+
+
+# singular values 0.003 .. 1 come out between 0.68 and 1.21 after five steps
+ORTHOGONALIZE_COEFFS = (3.4445, -4.7750, 2.0315)
+
+
+def moe_orthogonalize_workspace_bytes(B, m, n, out_dtype=torch.bfloat16) -> int:
+    return lib.moe_orthogonalize_workspace_bytes(B, m, n, dtype_code(out_dtype))
+
+
+def moe_orthogonalize(g, steps=5, coeffs=ORTHOGONALIZE_COEFFS, eps=1e-7, scale=1.0, out_dtype=None, out=None,
+                      workspace=None, stream=None):
+    """Orthogonalised update of every matrix of g [B, m, n] (or one [m, n]): ``steps`` of
+    X <- a X + (b A + c A A) X, A = X X^T, from X = g / (|g| + eps), times ``scale``.
+
+    g: float32 or bfloat16, contiguous (e.g. dw_gate of moe_grouped_ffn_backward).  out_dtype: bfloat16 (default;
+    one fp16 value per operand) or float32 (two, three products each)."""
+    fn = "moe_orthogonalize"
+    if g.dim() not in (2, 3):
+        raise ValueError(f"{fn}: g must be [B, m, n] or [m, n] (got {tuple(g.shape)})")
+    dev = g.device
+    B, m, n = g.shape if g.dim() == 3 else (1, *g.shape)
+    _tensor(fn, "g", g, g.shape, _ROW_TYPES, dev)
+    if len(coeffs) != 3:
+        raise ValueError(f"{fn}: coeffs are three numbers")
+    if out is not None and out_dtype is not None and out.dtype != out_dtype:
+        raise ValueError(f"{fn}: out has dtype {out.dtype}, not {out_dtype}")
+    ot = out.dtype if out is not None else out_dtype or torch.bfloat16
+    if ot not in _ROW_TYPES:
+        raise ValueError(f"{fn}: the output must be float32 or bfloat16 (got {ot})")
+    with _on_device(fn, dev, stream):
+        if out is None or workspace is None:
+            with _alloc_on(stream):
+                if out is None:
+                    out = torch.empty(g.shape, dtype=ot, device=dev)
+                if workspace is None:
+                    workspace = torch.empty(moe_orthogonalize_workspace_bytes(B, m, n, ot), dtype=torch.uint8,
+                                            device=dev)
+        _tensor(fn, "out", out, g.shape, (ot,), dev)
+        if g.numel() and out.untyped_storage().data_ptr() == g.untyped_storage().data_ptr():
+            a0, b0 = g.data_ptr(), out.data_ptr()
+            if a0 < b0 + _nbytes(out) and b0 < a0 + _nbytes(g):
+                raise ValueError(f"{fn}: out must not overlap g")
+        _workspace(fn, workspace, dev)
+        _check(lib.moe_orthogonalize(_ptr(g), dtype_code(g.dtype), B, m, n, steps, *coeffs, eps, scale, _ptr(out),
+                                     dtype_code(ot), _ptr(workspace), _nbytes(workspace), _stream(stream)), fn)
+    return out
+
+
 class MoELayer:
     """The four calls with buffers allocated once for a fixed (T, H, E, k, F) and dtype.
 
@@ -454,17 +682,27 @@ class MoELayer:
                  itself and the down product writes weighted pair-major slots that the combine sums;
       "gather"   the gate/up product gathers x rows itself (no x_perm), then the permuted down product and
                  combine: the same bits as "permuted" without the permuted copy of x.
-    ``train``: also keeps the natural-layout weights and the buffers of forward_train() / backward()."""
+    ``train``: also keeps the natural-layout weights and the buffers of forward_train() / backward().
+    ``norm`` ("layer" or "rms", with ``norm_weight`` [H] and, for "layer", optionally ``norm_bias``): the layer
+    normalises its rows itself: normalize() writes self.xn (e4m3 codes and scales for an fp8 layer, from bfloat16
+    rows) and forward_x() runs it in front of the router; normalize_backward() takes backward()'s dx through it."""
 
     FORMS = ("permuted", "fused", "gather")
 
     def __init__(self, T, H, E, k, F, dtype: torch.dtype, w_gate, w_up, w_down, s_gate=None, s_up=None, s_down=None,
-                 e_lo=0, out_dtype=None, device="cuda", fused=False, train=False, form=None):
+                 e_lo=0, out_dtype=None, device="cuda", fused=False, train=False, form=None, norm=None,
+                 norm_weight=None, norm_bias=None, norm_eps=1e-5):
         form = form or ("fused" if fused else "permuted")
         if form not in self.FORMS:
             raise ValueError(f"MoELayer: form {form!r} is not one of {self.FORMS}")
         if train and form != "permuted":
             raise ValueError("MoELayer: the training form uses the permuted layout (form='permuted')")
+        if norm is not None and norm not in NORM_KINDS:
+            raise ValueError(f"MoELayer: norm {norm!r} is not one of {tuple(NORM_KINDS)}")
+        if norm is not None and norm_weight is None:
+            raise ValueError("MoELayer: norm needs norm_weight")
+        if norm is None and (norm_weight is not None or norm_bias is not None):
+            raise ValueError("MoELayer: norm_weight and norm_bias need norm")
         self.form = form
         self.fused = form == "fused"
         gather_in = form != "permuted"
@@ -507,6 +745,65 @@ class MoELayer:
             desc = natural_weights(*self.w_nat)
             self.ws_bwd = torch.empty(lib.moe_grouped_ffn_backward_workspace_bytes(ctypes.byref(desc), R),
                                       dtype=torch.uint8, device=d)
+
+        self.norm, self.norm_weight, self.norm_bias, self.norm_eps = norm, norm_weight, norm_bias, norm_eps
+        if norm is not None:
+            self.row_dtype = torch.bfloat16 if self.fp8 else dtype
+            self.norm_rows = None  # the rows that normalize() took last
+            self.xn = torch.empty((T, H), dtype=dtype, device=d)
+            self.xn_scales = torch.empty((T, H // 128), dtype=torch.float32, device=d) if self.fp8 else None
+            self.row_sum = torch.empty((T, H), dtype=self.row_dtype, device=d)
+            self.row_mean = torch.empty(T, dtype=torch.float32, device=d) if norm == "layer" else None
+            self.row_rstd = torch.empty(T, dtype=torch.float32, device=d)
+            if train:
+                self.norm_grads = dict(dx=torch.empty((T, H), dtype=dtype, device=d),
+                                       dweight=torch.empty(H, dtype=torch.float32, device=d),
+                                       dbias=None if norm_bias is None
+                                       else torch.empty(H, dtype=torch.float32, device=d))
+                self.ws_norm = torch.empty(moe_norm_backward_workspace_bytes(T, H), dtype=torch.uint8, device=d)
+        self.updates = self.ws_orth = None
+
+    def _need(self, what, ok):
+        if not ok:
+            raise ValueError(f"MoELayer: {what}")
+
+    def normalize(self, x, residual=None, stream=None):
+        """The layer's norm of the rows x (+ residual): returns (xn, xn_scales or None).  self.norm_rows is then the
+        residual stream: x, or x + residual (a buffer of the layer)."""
+        self._need("normalize() needs a layer built with norm", self.norm is not None)
+        r = moe_norm(x, self.norm_weight, self.norm_bias, residual, self.norm, self.norm_eps, y=self.xn,
+                     y_scales=self.xn_scales, sum=self.row_sum, mean=self.row_mean, rstd=self.row_rstd, stream=stream)
+        self.norm_rows = r.sum
+        return self.xn, self.xn_scales
+
+    def normalize_backward(self, dxn, dsum=None, stream=None):
+        """Gradients through the last normalize(): dict(dx, dweight, dbias) of preallocated tensors.  dxn: gradient of
+        the normalised rows (backward()'s dx, with what the router's own product adds); dsum: gradient that reaches
+        the rows by the residual stream."""
+        self._need("normalize_backward() needs a layer built with norm and train=True",
+                   self.norm is not None and self.train)
+        self._need("normalize_backward() follows normalize()", self.norm_rows is not None)
+        return moe_norm_backward(dxn, self.norm_rows, self.norm_weight, self.row_mean, self.row_rstd, self.norm, dsum,
+                                 out=self.norm_grads, workspace=self.ws_norm, stream=stream)
+
+    def orthogonalize(self, steps=5, coeffs=ORTHOGONALIZE_COEFFS, eps=1e-7, scale=1.0, out_dtype=torch.bfloat16,
+                      stream=None):
+        """Orthogonalised updates of the last backward()'s weight gradients, one matrix per local expert: dict(w_gate,
+        w_up, w_down) of tensors that the layer keeps (as their workspace) from the first call on."""
+        self._need("orthogonalize() needs a layer built with train=True", self.train)
+        El, H, F = self.w_nat[0].shape
+        if self.updates is None or self.updates["w_gate"].dtype != out_dtype:
+            with _alloc_on(stream):
+                d = self.grads["dx"].device
+                self.updates = {k: torch.empty(self.grads["d" + k].shape, dtype=out_dtype, device=d)
+                                for k in ("w_gate", "w_up", "w_down")}
+                self.ws_orth = torch.empty(max(moe_orthogonalize_workspace_bytes(El, H, F, out_dtype),
+                                               moe_orthogonalize_workspace_bytes(El, F, H, out_dtype)),
+                                           dtype=torch.uint8, device=d)
+        for k, u in self.updates.items():
+            moe_orthogonalize(self.grads["d" + k], steps, coeffs, eps, scale, out=u, workspace=self.ws_orth,
+                              stream=stream)
+        return self.updates
 
     def forward_train(self, stream=None):
         """The grouped FFN keeping h and the pre-activations for backward() (after route and dispatch)."""
@@ -573,6 +870,18 @@ class MoELayer:
 
     def forward(self, logits, x, x_scales=None, stream=None):
         self.route(logits, stream)
+        self.dispatch(x, x_scales, stream)
+        self.ffn(stream)
+        return self.combine(stream)
+
+    def forward_x(self, x, w_router, x_scales=None, residual=None, stream=None):
+        """The layer from its rows: the norm (if the layer has one; residual is added first), the router's product and
+        top-k, dispatch, FFN, combine."""
+        if self.norm is not None:
+            x, x_scales = self.normalize(x, residual, stream)
+        else:
+            self._need("a residual needs a layer built with norm", residual is None)
+        self.route_x(x, w_router, x_scales, stream)
         self.dispatch(x, x_scales, stream)
         self.ffn(stream)
         return self.combine(stream)

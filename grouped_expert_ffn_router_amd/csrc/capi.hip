@@ -630,4 +630,189 @@ moe_status moe_combine(const float* y_perm, const int32_t* row_of_pair, const in
   return launch_status(fn);
 }
 
+// Checks shared by the two directions of the norm: sizes, types, row strides.
+static moe_status norm_sizes(const char* fn, moe_dtype dtype, moe_dtype w_dtype, int64_t T, int32_t H,
+                             moe_norm_kind kind) {
+  if (!dtype_ok(dtype) || !dtype_ok(w_dtype)) FAIL(MOE_ERR_INVALID_ARG, "%s: unknown dtype", fn);
+  if (dtype == MOE_DTYPE_FP8_E4M3 || w_dtype == MOE_DTYPE_FP8_E4M3)
+    FAIL(MOE_ERR_UNSUPPORTED, "%s: rows and parameters must be F32 or BF16", fn);
+  if (kind != MOE_NORM_LAYER && kind != MOE_NORM_RMS) FAIL(MOE_ERR_INVALID_ARG, "%s: unknown kind %d", fn, (int)kind);
+  if (T < 0 || T >= (1ll << 31)) FAIL(MOE_ERR_INVALID_ARG, "%s: T = %lld outside [0, 2^31)", fn, (long long)T);
+  if (H < 1 || H > 65536) FAIL(MOE_ERR_INVALID_ARG, "%s: H = %d outside [1, 65536]", fn, H);
+  return MOE_OK;
+}
+static bool ld_ok(int64_t ld, int32_t H) { return ld >= H && ld < (1ll << 31); }
+
+moe_status moe_norm(const void* x, int64_t ldx, const void* residual, int64_t ld_res, moe_dtype dtype, int64_t T,
+                    int32_t H, moe_norm_kind kind, const void* weight, const void* bias, moe_dtype w_dtype, float eps,
+                    void* sum, void* y, float* y_scales, moe_dtype y_dtype, float* mean, float* rstd,
+                    moe_stream stream) {
+  const char* fn = "moe_norm";
+  const moe_status st = norm_sizes(fn, dtype, w_dtype, T, H, kind);
+  if (st != MOE_OK) return st;
+  const bool fp8 = y_dtype == MOE_DTYPE_FP8_E4M3;
+  if (!dtype_ok(y_dtype)) FAIL(MOE_ERR_INVALID_ARG, "%s: unknown dtype %d", fn, (int)y_dtype);
+  if (!fp8 && y_dtype != dtype) FAIL(MOE_ERR_UNSUPPORTED, "%s: y_dtype must be the rows' dtype or FP8_E4M3", fn);
+  if (!(eps >= 0.0f && eps <= 3.4e38f)) FAIL(MOE_ERR_INVALID_ARG, "%s: eps = %g is negative or not finite", fn, (double)eps);
+  if (fp8 && H % 128) FAIL(MOE_ERR_INVALID_ARG, "%s: FP8_E4M3 needs H = %d to be a multiple of 128", fn, H);
+  if (!ld_ok(ldx, H) || (residual != nullptr && !ld_ok(ld_res, H)))
+    FAIL(MOE_ERR_INVALID_ARG, "%s: a row stride is outside [H, 2^31)", fn);
+  if (T == 0) return MOE_OK;
+  const size_t es = dtype_bytes(dtype), wes = dtype_bytes(w_dtype);
+  REQ_PTR(x, es, "x");
+  REQ_PTR(weight, wes, "weight");
+  REQ_PTR(y, fp8 ? 16 : es, "y");
+  if (bias != nullptr) REQ_PTR(bias, wes, "bias");
+  if (residual != nullptr) {
+    REQ_PTR(residual, es, "residual");
+    REQ_PTR(sum, es, "sum");
+  }
+  if (fp8) REQ_PTR(y_scales, 4, "y_scales");
+  if (mean != nullptr) REQ_PTR(mean, 4, "mean");
+  if (rstd != nullptr) REQ_PTR(rstd, 4, "rstd");
+  NormLaunch p{};
+  p.dtype = dtype;
+  p.T = T;
+  p.H = H;
+  p.rms = kind == MOE_NORM_RMS;
+  p.w_bf16 = w_dtype == MOE_DTYPE_BF16;
+  p.x = x;
+  p.ldx = ldx;
+  p.residual = residual;
+  p.ldr = residual != nullptr ? ld_res : 0;
+  p.weight = weight;
+  p.bias = bias;
+  p.eps = eps;
+  p.sum = residual != nullptr ? sum : nullptr;
+  p.y = y;
+  p.y_fp8 = fp8;
+  p.y_scales = y_scales;
+  p.mean = mean;
+  p.rstd = rstd;
+  if (fp8 && !norm_vector_ok(p))
+    FAIL(MOE_ERR_INVALID_ARG, "%s: FP8_E4M3 needs 16-byte aligned rows and parameters", fn);
+  launch_norm(p, (hipStream_t)stream);
+  return launch_status(fn);
+}
+
+size_t moe_norm_backward_workspace_bytes(int64_t T, int32_t H) {
+  if (T < 0 || T >= (1ll << 31) || H < 1 || H > 65536) return 0;
+  return align256(2 * (size_t)norm_backward_groups(T, H) * (size_t)H * sizeof(float)) + 256;
+}
+
+moe_status moe_norm_backward(const void* dy, int64_t ld_dy, const void* s, int64_t ld_s, const void* dsum,
+                             int64_t ld_dsum, moe_dtype dtype, int64_t T, int32_t H, moe_norm_kind kind,
+                             const void* weight, moe_dtype w_dtype, const float* mean, const float* rstd, void* dx,
+                             float* dweight, float* dbias, void* workspace, size_t workspace_bytes,
+                             moe_stream stream) {
+  const char* fn = "moe_norm_backward";
+  const moe_status st = norm_sizes(fn, dtype, w_dtype, T, H, kind);
+  if (st != MOE_OK) return st;
+  if (!ld_ok(ld_dy, H) || !ld_ok(ld_s, H) || (dsum != nullptr && !ld_ok(ld_dsum, H)))
+    FAIL(MOE_ERR_INVALID_ARG, "%s: a row stride is outside [H, 2^31)", fn);
+  REQ_PTR(dweight, 4, "dweight");
+  if (dbias != nullptr) REQ_PTR(dbias, 4, "dbias");
+  if (T > 0) {
+    const size_t es = dtype_bytes(dtype);
+    REQ_PTR(dy, es, "dy");
+    REQ_PTR(s, es, "s");
+    if (dsum != nullptr) REQ_PTR(dsum, es, "dsum");
+    REQ_PTR(weight, dtype_bytes(w_dtype), "weight");
+    if (kind == MOE_NORM_LAYER) REQ_PTR(mean, 4, "mean");
+    REQ_PTR(rstd, 4, "rstd");
+    REQ_PTR(dx, es, "dx");
+    const size_t need = moe_norm_backward_workspace_bytes(T, H);
+    if (workspace == nullptr || workspace_bytes < need || !aligned(workspace, 256))
+      FAIL(MOE_ERR_WORKSPACE, "%s: workspace needs %zu bytes, 256-byte aligned (got %zu)", fn, need, workspace_bytes);
+  }
+  NormLaunch p{};
+  p.dtype = dtype;
+  p.T = T;
+  p.H = H;
+  p.rms = kind == MOE_NORM_RMS;
+  p.w_bf16 = w_dtype == MOE_DTYPE_BF16;
+  p.x = s;
+  p.ldx = ld_s;
+  p.residual = dsum;
+  p.ldr = dsum != nullptr ? ld_dsum : 0;
+  p.weight = weight;
+  p.mean = const_cast<float*>(mean);
+  p.rstd = const_cast<float*>(rstd);
+  p.dy = dy;
+  p.ld_dy = ld_dy;
+  p.dx = dx;
+  p.dweight = dweight;
+  p.dbias = dbias;
+  p.part = reinterpret_cast<float*>(workspace);
+  launch_norm_backward(p, (hipStream_t)stream);
+  return launch_status(fn);
+}
+
+size_t moe_orthogonalize_workspace_bytes(int64_t batch, int32_t m, int32_t n, moe_dtype out_dtype) {
+  if (batch < 1 || batch >= (1 << 24) || m < 1 || n < 1 || m > 65536 || n > 65536) return 0;
+  return orthogonalize_workspace(batch, m, n, out_dtype == MOE_DTYPE_BF16);
+}
+
+// Whether `steps` of s -> s (a + b s^2 + c s^4) from [0, 1] stay where the fp16 operands hold them: |s| <= 3, and
+// |b s^2 + c s^4| <= 12 (the operands carry a factor 2^12, and fp16 ends at 16 * 2^12).  The bounds are taken at 4097
+// points of each step's interval, with a factor 1.01 between steps for what lies between the points.
+static bool iteration_bounded(int32_t steps, float a, float b, float c) {
+  double hi = 1.0;
+  for (int32_t k = 0; k < steps; ++k) {
+    double next = 0.0;
+    for (int i = 0; i <= 4096; ++i) {
+      const double s = hi * i / 4096, s2 = s * s, q = (double)b * s2 + (double)c * s2 * s2;
+      const double v = s * ((double)a + q);
+      if (!(q <= 12.0 && q >= -12.0 && v <= 3.0 && v >= -3.0)) return false;
+      next = v > next ? v : (-v > next ? -v : next);
+    }
+    hi = next * 1.01;
+  }
+  return true;
+}
+
+moe_status moe_orthogonalize(const void* g, moe_dtype g_dtype, int64_t batch, int32_t m, int32_t n, int32_t steps,
+                             float a, float b, float c, float eps, float scale, void* out, moe_dtype out_dtype,
+                             void* workspace, size_t workspace_bytes, moe_stream stream) {
+  const char* fn = "moe_orthogonalize";
+  if (!dtype_ok(g_dtype) || !dtype_ok(out_dtype)) FAIL(MOE_ERR_INVALID_ARG, "%s: unknown dtype", fn);
+  if (g_dtype == MOE_DTYPE_FP8_E4M3 || out_dtype == MOE_DTYPE_FP8_E4M3)
+    FAIL(MOE_ERR_UNSUPPORTED, "%s: g and out must be F32 or BF16", fn);
+  if (batch < 0 || batch >= (1 << 24)) FAIL(MOE_ERR_INVALID_ARG, "%s: batch = %lld outside [0, 2^24)", fn, (long long)batch);
+  if (m < 1 || n < 1 || m > 65536 || n > 65536)
+    FAIL(MOE_ERR_INVALID_ARG, "%s: m = %d or n = %d outside [1, 65536]", fn, m, n);
+  if (steps < 1 || steps > 32) FAIL(MOE_ERR_INVALID_ARG, "%s: steps = %d outside [1, 32]", fn, steps);
+  if (!(eps > 0.0f && eps <= 3.4e38f)) FAIL(MOE_ERR_INVALID_ARG, "%s: eps = %g is not positive and finite", fn, (double)eps);
+  if (!(scale >= -3.4e38f && scale <= 3.4e38f)) FAIL(MOE_ERR_INVALID_ARG, "%s: scale is not finite", fn);
+  if (!iteration_bounded(steps, a, b, c))
+    FAIL(MOE_ERR_INVALID_ARG, "%s: the coefficients (%g, %g, %g) do not keep %d steps bounded", fn, (double)a, (double)b,
+         (double)c, steps);
+  // tiles of 128 x 128 over the whole batch are one grid
+  const int64_t tiles = ((m + 255) / 256 * 2) * (int64_t)((n + 255) / 256 * 2);
+  if (tiles * batch >= (1ll << 28)) FAIL(MOE_ERR_INVALID_ARG, "%s: batch * m * n is too large for one launch", fn);
+  if (batch == 0) return MOE_OK;
+  REQ_PTR(g, dtype_bytes(g_dtype), "g");
+  REQ_PTR(out, dtype_bytes(out_dtype), "out");
+  const size_t need = moe_orthogonalize_workspace_bytes(batch, m, n, out_dtype);
+  if (workspace == nullptr || workspace_bytes < need || !aligned(workspace, 256))
+    FAIL(MOE_ERR_WORKSPACE, "%s: workspace needs %zu bytes, 256-byte aligned (got %zu)", fn, need, workspace_bytes);
+  OrthLaunch p{};
+  p.g = g;
+  p.g_bf16 = g_dtype == MOE_DTYPE_BF16;
+  p.batch = batch;
+  p.m = m;
+  p.n = n;
+  p.steps = steps;
+  p.a = a;
+  p.b = b;
+  p.c = c;
+  p.eps = eps;
+  p.scale = scale;
+  p.out = out;
+  p.out_bf16 = out_dtype == MOE_DTYPE_BF16;
+  p.workspace = workspace;
+  launch_orthogonalize(p, (hipStream_t)stream);
+  return launch_status(fn);
+}
+
 }  // extern "C"

@@ -8,8 +8,10 @@
 #define MOE_DEV __device__ __forceinline__
 
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
+typedef int i32x2_t __attribute__((ext_vector_type(2)));
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
 
@@ -24,6 +26,10 @@ MOE_DEV int lane_id() { return (int)__lane_id(); }
 // template kernel never sees a target-specific builtin.
 MOE_DEV f32x16_t mfma_32x32x16_bf16(bf16x8_t a, bf16x8_t b, f32x16_t c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+MOE_DEV f32x16_t mfma_32x32x16(bf16x8_t a, bf16x8_t b, f32x16_t c) { return mfma_32x32x16_bf16(a, b, c); }
+MOE_DEV f32x16_t mfma_32x32x16(f16x8_t a, f16x8_t b, f32x16_t c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
 }
 MOE_DEV f32x16_t mfma_32x32x2_f32(float a, float b, f32x16_t c) {
   return __builtin_amdgcn_mfma_f32_32x32x2f32(a, b, c, 0, 0, 0);

@@ -170,9 +170,9 @@ MOE_DEV i32x4_t lds_at(lds_u8_t* p, int imm) { return *(lds_i32x4_t*)(p + imm); 
 // are compile-time multiples of 16 after inlining.
 // ---------------------------------------------------------------------------------------------------------
 
-// bf16: k-steps of 16 (one 16-byte chunk per lane half); fragments double-buffered in registers so step s+1's LDS
+// bf16 (V = bf16x8_t) or fp16 (f16x8_t): k-steps of 16 (one 16-byte chunk per lane half); fragments double-buffered in registers so step s+1's LDS
 // reads overlap step s's MFMAs, interleaved one LDS read per group of MFMAs.
-template <int RB, int MB, int NB>
+template <int RB, int MB, int NB, typename V = bf16x8_t>
 MOE_DEV void mma_stage_bf16(const uint8_t* As, const uint8_t* Bs, const int (&arow)[MB], const int (&brow)[NB],
                             const FragOff& ao, const FragOff& bo,
                             f32x16_t (&acc)[MB][NB]) {
@@ -184,11 +184,11 @@ MOE_DEV void mma_stage_bf16(const uint8_t* As, const uint8_t* Bs, const int (&ar
     av[s] = to_lds(As) + ao.o[s];
     bv[s] = to_lds(Bs) + bo.o[s];
   }
-  bf16x8_t fa[2][MB], fb[2][NB];
+  V fa[2][MB], fb[2][NB];
 #pragma unroll
-  for (int i = 0; i < MB; ++i) fa[0][i] = __builtin_bit_cast(bf16x8_t, lds_at(av[0], (arow[i] - arow[0]) * RB));
+  for (int i = 0; i < MB; ++i) fa[0][i] = __builtin_bit_cast(V, lds_at(av[0], (arow[i] - arow[0]) * RB));
 #pragma unroll
-  for (int j = 0; j < NB; ++j) fb[0][j] = __builtin_bit_cast(bf16x8_t, lds_at(bv[0], (brow[j] - brow[0]) * RB));
+  for (int j = 0; j < NB; ++j) fb[0][j] = __builtin_bit_cast(V, lds_at(bv[0], (brow[j] - brow[0]) * RB));
   sched_fence();
 #pragma unroll
   for (int s = 0; s < NSTEP; ++s) {
@@ -196,15 +196,15 @@ MOE_DEV void mma_stage_bf16(const uint8_t* As, const uint8_t* Bs, const int (&ar
     if (s + 1 < NSTEP) {
 #pragma unroll
       for (int i = 0; i < MB; ++i)
-        fa[c ^ 1][i] = __builtin_bit_cast(bf16x8_t, lds_at(av[s + 1], (arow[i] - arow[0]) * RB));
+        fa[c ^ 1][i] = __builtin_bit_cast(V, lds_at(av[s + 1], (arow[i] - arow[0]) * RB));
 #pragma unroll
       for (int j = 0; j < NB; ++j)
-        fb[c ^ 1][j] = __builtin_bit_cast(bf16x8_t, lds_at(bv[s + 1], (brow[j] - brow[0]) * RB));
+        fb[c ^ 1][j] = __builtin_bit_cast(V, lds_at(bv[s + 1], (brow[j] - brow[0]) * RB));
     }
 #pragma unroll
     for (int i = 0; i < MB; ++i)
 #pragma unroll
-      for (int j = 0; j < NB; ++j) acc[i][j] = mfma_32x32x16_bf16(fa[c][i], fb[c][j], acc[i][j]);
+      for (int j = 0; j < NB; ++j) acc[i][j] = mfma_32x32x16(fa[c][i], fb[c][j], acc[i][j]);
     if (s + 1 < NSTEP) {
       constexpr int PER = (MB * NB) / (MB + NB) > 0 ? (MB * NB) / (MB + NB) : 1;
 #pragma unroll

@@ -75,4 +75,46 @@ void launch_combine(const float* y, const int32_t* rop, const int32_t* idx, cons
 void launch_combine_slots(const float* y_slot, const int32_t* rop, const int32_t* idx, int64_t T, int k, int H,
                           int e_lo, int E_local, void* out, bool out_bf16, hipStream_t s);
 
+// Layer norm / RMS norm of token rows (norm.hip).
+struct NormLaunch {
+  moe_dtype dtype;  // rows: F32 or BF16
+  int64_t T;
+  int H;
+  bool rms, w_bf16;
+  const void* x;  // forward: input rows; backward: the rows that were normalised
+  int64_t ldx;
+  const void* residual;  // forward: added to x, or NULL; backward: gradient of those rows from elsewhere, or NULL
+  int64_t ldr;
+  const void *weight, *bias;
+  float eps;
+  void* sum;        // forward with residual: x + residual
+  void* y;          // forward
+  bool y_fp8;
+  float* y_scales;  // y_fp8: [T][H/128]
+  float *mean, *rstd;
+  const void* dy;  // backward
+  int64_t ld_dy;
+  void* dx;
+  float *dweight, *dbias;
+  float* part;  // workspace: [2][norm_backward_groups][H]
+};
+int norm_backward_groups(int64_t T, int H);
+bool norm_vector_ok(const NormLaunch& p);  // whether every operand takes 16-byte accesses
+void launch_norm(const NormLaunch& p, hipStream_t s);
+void launch_norm_backward(const NormLaunch& p, hipStream_t s);
+
+// Orthogonalised updates (orthogonalize.hip).
+struct OrthLaunch {
+  const void* g;
+  bool g_bf16;
+  int64_t batch;
+  int m, n, steps;
+  float a, b, c, eps, scale;
+  void* out;
+  bool out_bf16;
+  void* workspace;
+};
+size_t orthogonalize_workspace(int64_t batch, int m, int n, bool out_bf16);
+void launch_orthogonalize(const OrthLaunch& p, hipStream_t s);
+
 }  // namespace moe

@@ -16,6 +16,8 @@
  *   fixed capacity per expert (pairs past it dropped)                             -> moe_dispatch_permute_capacity
  *   training: the forward keeping its activations, then the gradients of x, the expert weights, the routing
  *   weights and the logits                        -> moe_grouped_ffn_train, moe_grouped_ffn_backward
+ *   around it: the norm of the rows that enter the layer and its gradients, and the update made of the expert
+ *   weights' gradients                            -> moe_norm, moe_norm_backward, moe_orthogonalize
  * Between ranks, steps 2 and 4 are all-to-all exchanges; on one GPU they are the local permutation and its
  * inverse, and the exchange itself is not part of this library.
  *
@@ -360,6 +362,74 @@ moe_status moe_grouped_ffn_backward(const void* dout, int64_t T, int32_t k, int3
                                     const void* h, const float* gu, const float* y_perm, const moe_ffn_weights* w,
                                     void* dx, float* dw_gate, float* dw_up, float* dw_down, float* d_topk_w,
                                     float* d_logits, void* workspace, size_t workspace_bytes, moe_stream stream);
+
+/*
+ * Norm of the rows that enter the layer.  For each row t of H values:
+ *   s = x[t], or x[t] + residual[t] rounded once to dtype (the stored sum is what is normalised)
+ *   m = mean(s) for MOE_NORM_LAYER, 0 for MOE_NORM_RMS;  r = 1 / sqrt(mean((s - m)^2) + eps)
+ *   y[t] = (s - m) r weight [+ bias]
+ * Statistics and products in fp32, one rounding of y.
+ *   x        (device) [T, H] in dtype (F32 or BF16), rows ldx elements apart (ldx >= H).
+ *   residual (device) [T, H] in dtype, rows ld_res elements apart, or NULL.
+ *   weight, bias (device) [H] in w_dtype (F32 or BF16); bias may be NULL.
+ *   sum      (device) [T, H] in dtype out, contiguous: s; required with residual, unused without.  It may be x or
+ *            residual itself (contiguous rows); outputs overlap no input otherwise.
+ *   y        (device) [T, H] contiguous out, y_dtype: dtype, or FP8_E4M3 with y_scales (device) [T, H/128] fp32 out,
+ *            the form moe_dispatch_permute takes: per row and 128 columns scale = amax / 448 (amax over the values
+ *            that are not NaN; 1 where amax is 0), code = y / scale rounded to nearest even, NaN kept.  FP8_E4M3
+ *            needs H % 128 == 0 and 16-byte aligned rows and parameters.  y_scales is unused otherwise.
+ *   mean, rstd (device) [T] fp32 out, each may be NULL; mean is not written for MOE_NORM_RMS.
+ * Alignment: the element size (16-byte aligned rows and parameters take wide accesses).
+ * Domain: 0 <= T < 2^31, 1 <= H <= 65536, eps >= 0 and finite.
+ */
+typedef enum { MOE_NORM_LAYER = 0, MOE_NORM_RMS = 1 } moe_norm_kind;
+moe_status moe_norm(const void* x, int64_t ldx, const void* residual, int64_t ld_res, moe_dtype dtype, int64_t T,
+                    int32_t H, moe_norm_kind kind, const void* weight, const void* bias, moe_dtype w_dtype, float eps,
+                    void* sum, void* y, float* y_scales, moe_dtype y_dtype, float* mean, float* rstd,
+                    moe_stream stream);
+
+/*
+ * Gradients of moe_norm for dy = dL/dy.  With z = (s - mean) rstd and t = dy weight:
+ *   dx      = rstd (t - [mean(t)] - z mean(t z)) [+ dsum]   (the bracketed mean for MOE_NORM_LAYER only)
+ *   dweight = sum over rows of dy z,   dbias = sum over rows of dy
+ * dx is the gradient of s, hence of x and of residual alike; dsum is the gradient that reaches s by another way (the
+ * residual stream), added before the one rounding of dx.  Sums in fp32, in an order set by T and H alone (no atomics).
+ *   dy, s, dsum (device) [T, H] in dtype, rows ld_* elements apart; s is moe_norm's sum (or x without residual);
+ *               dsum may be NULL.
+ *   mean, rstd  (device) [T] fp32 from moe_norm (mean unused for MOE_NORM_RMS).
+ *   dx          (device) [T, H] in dtype out, contiguous; may be dy or dsum itself (contiguous rows).
+ *   dweight, dbias (device) [H] fp32 out, written (not added to); dbias may be NULL.  T = 0 writes zeros.
+ *   workspace   (device) at least moe_norm_backward_workspace_bytes(T, H) bytes, 256-byte aligned.
+ * Domain and alignment as moe_norm.
+ */
+size_t moe_norm_backward_workspace_bytes(int64_t T, int32_t H);
+moe_status moe_norm_backward(const void* dy, int64_t ld_dy, const void* s, int64_t ld_s, const void* dsum,
+                             int64_t ld_dsum, moe_dtype dtype, int64_t T, int32_t H, moe_norm_kind kind,
+                             const void* weight, moe_dtype w_dtype, const float* mean, const float* rstd, void* dx,
+                             float* dweight, float* dbias, void* workspace, size_t workspace_bytes, moe_stream stream);
+
+/*
+ * Orthogonalised update of `batch` matrices (the gradients, or momenta, of the expert weights) by `steps`
+ * Newton-Schulz steps.  For each matrix g of m x n, on the side that makes X no taller than wide:
+ *   X = g / (|g|_F + eps);   steps times:  A = X X^T,  X = a X + (b A + c A A) X;   out = scale X
+ * which moves every singular value s of X through s -> a s + b s^3 + c s^5, the singular vectors kept.
+ *   g    (device) [batch, m, n] in g_dtype (F32 or BF16).  |g|_F is summed in fp64.  A matrix of zeros gives zeros; one
+ *        with an infinity or a NaN gives NaN, and touches no other matrix of the batch.
+ *   out  (device) [batch, m, n] out, out_dtype F32 or BF16; must not overlap g.
+ * Precision: products of fp16 operands accumulated in fp32, X kept to 22 bits between the steps.  out_dtype BF16 takes
+ * each operand to one fp16 value, scaled so that none is subnormal in earnest: |error|_F is about 1.5e-3 |out|_F, as
+ * the rounding to bf16 itself.  F32 takes each operand to two (hi + lo, 22 bits) and three products: fp32's accuracy at
+ * three times the products' cost.
+ *   X's values are held to 2^-37 at least: a g whose norm is below about 1e-9 eps gives zeros.
+ *   workspace (device) at least moe_orthogonalize_workspace_bytes(batch, m, n, out_dtype) bytes, 256-byte aligned.
+ * Domain: batch >= 0, 1 <= m, n <= 65536, 1 <= steps <= 32, eps > 0 and finite, scale finite, and coefficients that keep
+ * the iteration bounded: from singular values in [0, 1] every step's stay within 3, and those of b A + c A A within 12
+ * (MOE_ERR_INVALID_ARG otherwise).  Results do not depend on run or launch order.
+ */
+size_t moe_orthogonalize_workspace_bytes(int64_t batch, int32_t m, int32_t n, moe_dtype out_dtype);
+moe_status moe_orthogonalize(const void* g, moe_dtype g_dtype, int64_t batch, int32_t m, int32_t n, int32_t steps,
+                             float a, float b, float c, float eps, float scale, void* out, moe_dtype out_dtype,
+                             void* workspace, size_t workspace_bytes, moe_stream stream);
 
 /*
  * Host-only helper: the dispatch + combine payload in bytes of `tokens` tokens for one MoE layer, the closed
