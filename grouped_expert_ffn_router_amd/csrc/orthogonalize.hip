@@ -4,7 +4,9 @@
 //
 // Three matrix products a step.  A and A A are symmetric, so only the tiles on and above the diagonal are computed and
 // each is stored twice, once transposed: p^2 q + p^3 + 2 p^2 q operations a step instead of 2 p^2 q + 2 p^3 + 2 p^2 q.
-// Bound by the matrix instructions: a step at p = 2048, q = 7168 is 99 GFLOP on 59 MB.
+// Bound by the matrix instructions: a step at p = 2048, q = 7168 is 99 GFLOP on 59 MB.  A product whose tiles do not fill
+// the last round of the 256 compute units shares those tiles' reductions among workgroups and joins them in a launch of its
+// own (8 x 2048 x 7168: 288 tiles of 256 x 256, X X^T from 369 to 264 + 14 us); see shape().
 //
 // Number formats.  Operands are fp16 (11 bits; the products then run at the bf16 rate with an eighth of its rounding
 // error), accumulated in fp32.  Everything carries a factor S = 2^12: entries of an orthogonal-like p x q matrix are near
@@ -33,24 +35,43 @@ constexpr float S = 4096.0f;
 
 enum Mode { GRAM = 0, POLY = 1, UPDATE = 2, FINAL = 3 };
 
-// 256 x 256 tiles over 8 wavefronts (128 x 64 each), two stages of 64 reduction values; 128 x 128 over 4 wavefronts
-// (64 x 64 each), four stages of 32 values: two workgroups share a compute unit.
-template <int BIG>
+// Tiles.  0: 64 x 64 over 4 wavefronts (32 x 32 each); 1: 128 x 128 over 4 (64 x 64 each); 2: 256 x 256 over 8
+// (128 x 64 each).  A stage holds RB bytes of the reduction for every tile row of each operand array (hi, and lo with
+// SPLIT); NS stages are in flight or in use.  The small tiles' stages leave room for a second workgroup on a compute unit:
+// with SPLIT two stages of 64 x 64 instead of four took three matrices of 1001 x 333 from 186 to 163 us.
+template <int SIZE, bool SPLIT>
 struct Cfg;
 template <>
-struct Cfg<0> {
-  static constexpr int RB = 64, NS = 4, BM = 128, BN = 128, WM = 2, WN = 2;
+struct Cfg<0, false> {
+  static constexpr int RB = 128, NS = 3, B = 64, WM = 2, WN = 2;
 };
 template <>
-struct Cfg<1> {
-  static constexpr int RB = 128, NS = 2, BM = 256, BN = 256, WM = 2, WN = 4;
+struct Cfg<1, false> {
+  static constexpr int RB = 64, NS = 4, B = 128, WM = 2, WN = 2;
 };
+template <>
+struct Cfg<2, false> {
+  static constexpr int RB = 128, NS = 2, B = 256, WM = 2, WN = 4;
+};
+template <>
+struct Cfg<0, true> {
+  static constexpr int RB = 128, NS = 2, B = 64, WM = 2, WN = 2;
+};
+template <>
+struct Cfg<1, true> {
+  static constexpr int RB = 64, NS = 2, B = 128, WM = 2, WN = 2;
+};
+template <>
+struct Cfg<2, true> {
+  static constexpr int RB = 64, NS = 2, B = 256, WM = 2, WN = 4;
+};
+constexpr int TILE[3] = {64, 128, 256};
 
 struct Args {
   // operands: hi and (SPLIT) lo, [rows][K] fp16 per matrix of the batch
   const uint8_t *M0, *M1, *N0, *N1;
   int64_t m_batch, n_batch;  // bytes between matrices
-  int K;                     // reduction length (values), a multiple of the tile size
+  int K;                     // reduction length (values), a multiple of 64
   int mt, nt;                // row and column tiles (symmetric products: mt == nt)
   // results and the elementwise operand: hi and lo, [rows][ld]; the transposed result T0 (T1: SPLIT) [cols][ld_t]
   const uint8_t *E0, *E1;
@@ -58,6 +79,9 @@ struct Args {
   int ld, ld_t;
   int64_t r_batch, t_batch;  // bytes between matrices
   float alpha, beta;         // result = alpha * E + beta * product
+  // the first `whole` tiles are one workgroup each; `parts` workgroups share each of the rest
+  int whole, parts;
+  float* partial;            // [rest * parts][tile values]
   // FINAL: out [m][n], row i of X is row i of out (flip: column i)
   uint8_t* out;
   int m, n;
@@ -75,84 +99,258 @@ MOE_DEV void wave_lds_fence() {
   __builtin_amdgcn_wave_barrier();
 }
 
-template <int MODE, int BIG, bool SPLIT>
-__global__ __launch_bounds__((64 * Cfg<BIG>::WM * Cfg<BIG>::WN)) void product_kernel(const Args a) {
-  using C_ = Cfg<BIG>;
-  constexpr int RB = C_::RB, NS = C_::NS, BM = C_::BM, BN = C_::BN, WM = C_::WM, WN = C_::WN, NW = WM * WN;
-  constexpr int WTM = BM / WM, WTN = BN / WN, MB = WTM / 32, NB = WTN / 32;
-  constexpr int RPI = 1024 / RB;  // rows one wavefront load instruction fills
-  constexpr int A_INS = BM / (NW * RPI), B_INS = BN / (NW * RPI), NL = A_INS + B_INS;
-  constexpr int STAGE = (BM + BN) * RB, CPR = RB / 16;
-  constexpr int PITCH = 68;  // floats per row of a wavefront's 32 x 64 epilogue block
-  constexpr int SMEM = NS * STAGE > NW * 32 * PITCH * 4 ? NS * STAGE : NW * 32 * PITCH * 4;
-  constexpr bool SYM = MODE == GRAM || MODE == POLY;
+// One stage with both operands as hi + lo: acc += lo hi + hi lo + hi hi.  The lo rows follow the hi rows of an operand at
+// a_lo / b_lo bytes.
+template <int RB, int MB, int NB>
+MOE_DEV void mma_stage_split(const uint8_t* As, const uint8_t* Bs, int a_lo, int b_lo, const int (&arow)[MB],
+                             const int (&brow)[NB], const tile::FragOff& ao, const tile::FragOff& bo,
+                             f32x16_t (&acc)[MB][NB]) {
+#pragma unroll
+  for (int s = 0; s < RB / 32; ++s) {
+    tile::lds_u8_t* av = tile::to_lds(As) + ao.o[s];
+    tile::lds_u8_t* bv = tile::to_lds(Bs) + bo.o[s];
+    f16x8_t bh[NB], bl[NB];
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+      bh[j] = __builtin_bit_cast(f16x8_t, tile::lds_at(bv, (brow[j] - brow[0]) * RB));
+      bl[j] = __builtin_bit_cast(f16x8_t, tile::lds_at(bv, b_lo + (brow[j] - brow[0]) * RB));
+    }
+#pragma unroll
+    for (int i = 0; i < MB; ++i) {
+      const f16x8_t ah = __builtin_bit_cast(f16x8_t, tile::lds_at(av, (arow[i] - arow[0]) * RB));
+      const f16x8_t al = __builtin_bit_cast(f16x8_t, tile::lds_at(av, a_lo + (arow[i] - arow[0]) * RB));
+#pragma unroll
+      for (int j = 0; j < NB; ++j) acc[i][j] = mfma_32x32x16(al, bh[j], acc[i][j]);
+#pragma unroll
+      for (int j = 0; j < NB; ++j) acc[i][j] = mfma_32x32x16(ah, bl[j], acc[i][j]);
+#pragma unroll
+      for (int j = 0; j < NB; ++j) acc[i][j] = mfma_32x32x16(ah, bh[j], acc[i][j]);
+    }
+  }
+}
+
+struct TileAt {
+  int e, mi, ni;  // matrix, row tile, column tile
+};
+template <int MODE>
+MOE_DEV TileAt tile_at(const Args& a, int L) {
+  TileAt r;
+  if constexpr (MODE == GRAM || MODE == POLY) {
+    // tile t of the upper triangle, column by column: t = ni (ni + 1) / 2 + mi, mi <= ni
+    const int per = a.nt * (a.nt + 1) / 2;
+    r.e = L / per;
+    const int t = L % per;
+    r.ni = (int)((sqrtf(8.0f * (float)t + 1.0f) - 1.0f) * 0.5f);
+    while (r.ni * (r.ni + 1) / 2 > t) --r.ni;
+    while ((r.ni + 1) * (r.ni + 2) / 2 <= t) ++r.ni;
+    r.mi = t - r.ni * (r.ni + 1) / 2;
+  } else {
+    // groups of 4 row tiles, column tiles next, row tiles fastest: the tiles that an XCD runs at once share operands
+    const int per = a.mt * a.nt;
+    r.e = L / per;
+    const int t = L % per;
+    const int g = t / (4 * a.nt), q = t % (4 * a.nt);
+    const int gm = min(4, a.mt - g * 4);
+    r.ni = q / gm;
+    r.mi = g * 4 + q % gm;
+  }
+  r.e = uniform_int(r.e);
+  r.mi = uniform_int(r.mi);
+  r.ni = uniform_int(r.ni);
+  return r;
+}
+
+// What follows a product for one 32 x W block of a wavefront (W = WTN columns), through the wavefront's own LDS block, so
+// that every global access is 16 bytes per lane: by rows for the result (and the elementwise operand, loaded ahead by the
+// caller), by columns for the transpose.
+// Accumulator element v of a lane: row (v / 4) * 8 + 4 * (lane / 32) + v % 4, column lane % 32.
+template <int MODE, int W, bool SPLIT>
+struct Epilogue {
+  static constexpr bool SYM = MODE == GRAM || MODE == POLY;
+  static constexpr bool HAS_E = MODE != GRAM, E_LO = MODE == UPDATE || MODE == FINAL || (MODE == POLY && SPLIT);
+  static constexpr int NB = W / 32, PITCH = W + 4;                       // floats per row of the LDS block
+  static constexpr int LPR = W / 8, RPP = 64 / LPR, PASS = 32 / RPP;     // lanes per row, rows per pass, passes
+  struct Elem {
+    f16x8_t h[HAS_E ? PASS : 1], l[E_LO ? PASS : 1];
+  };
+
+  static MOE_DEV void load(const Args& a, int e, int row0, int col0, Elem& x) {
+    if constexpr (HAS_E) {
+      const int lane = threadIdx.x & 63;
+#pragma unroll
+      for (int it = 0; it < PASS; ++it) {
+        const int64_t at = e * a.r_batch + ((int64_t)(row0 + it * RPP + lane / LPR) * a.ld + col0 + lane % LPR * 8) * 2;
+        x.h[it] = *reinterpret_cast<const f16x8_t*>(a.E0 + at);
+        if constexpr (E_LO) x.l[it] = *reinterpret_cast<const f16x8_t*>(a.E1 + at);
+      }
+    }
+  }
+
+  static MOE_DEV void store_out(const Args& a, int64_t o, int gc, const float (&v)[8]) {
+#pragma unroll
+    for (int x = 0; x < 8; ++x)
+      if (gc + x < a.n) {
+        if (a.out_bf16)
+          reinterpret_cast<uint16_t*>(a.out)[o + x] = f32_to_bf16_bits(v[x]);
+        else
+          reinterpret_cast<float*>(a.out)[o + x] = v[x];
+      }
+  }
+  static MOE_DEV void store_out8(const Args& a, int64_t o, const float (&v)[8]) {
+    if (a.out_bf16) {
+      i32x4_t w;
+#pragma unroll
+      for (int d = 0; d < 4; ++d)
+        w[d] = (int)((uint32_t)f32_to_bf16_bits(v[2 * d]) | ((uint32_t)f32_to_bf16_bits(v[2 * d + 1]) << 16));
+      *reinterpret_cast<i32x4_t*>(a.out + o * 2) = w;
+    } else {
+#pragma unroll
+      for (int d = 0; d < 2; ++d)
+        *reinterpret_cast<f32x4_t*>(a.out + o * 4 + 16 * d) =
+            (f32x4_t){v[4 * d], v[4 * d + 1], v[4 * d + 2], v[4 * d + 3]};
+    }
+  }
+  static MOE_DEV void store_pair(uint8_t* p0, uint8_t* p1, bool lo_too, int64_t at, const float (&v)[8]) {
+    f16x8_t h, l;
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+      _Float16 hi, lo;
+      split16(v[x], hi, lo);
+      h[x] = hi;
+      l[x] = lo;
+    }
+    *reinterpret_cast<f16x8_t*>(p0 + at) = h;
+    if (lo_too) *reinterpret_cast<f16x8_t*>(p1 + at) = l;
+  }
+
+  // block at (row0, col0) of matrix e; mirror: also store it transposed
+  static MOE_DEV void run(const Args& a, int e, int row0, int col0, bool mirror, const f32x16_t (&acc)[NB], const Elem& el,
+                          float* sc) {
+    const int lane = threadIdx.x & 63, lr = lane & 31, lh = lane >> 5;
+#pragma unroll
+    for (int j = 0; j < NB; ++j)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) sc[((v >> 2) * 8 + 4 * lh + (v & 3)) * PITCH + j * 32 + lr] = acc[j][v];
+    wave_lds_fence();
+    const bool turn = MODE == FINAL ? a.flip : mirror;
+#pragma unroll
+    for (int it = 0; it < PASS; ++it) {
+      const int r = it * RPP + lane / LPR, c = lane % LPR * 8;
+      float v[8];
+#pragma unroll
+      for (int d = 0; d < 2; ++d) {
+        const f32x4_t q = *reinterpret_cast<const f32x4_t*>(&sc[r * PITCH + c + 4 * d]);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) v[4 * d + x] = a.beta * q[x];
+      }
+      if constexpr (HAS_E) {
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          float ev = (float)el.h[it][x];
+          if constexpr (E_LO) ev += (float)el.l[it][x];
+          v[x] = __builtin_fmaf(a.alpha, ev, v[x]);
+        }
+      }
+      if constexpr (MODE == FINAL) {
+        const int gr = row0 + r, gc = col0 + c;
+        if (!a.flip && gr < a.m && gc < a.n) {
+          const int64_t o = ((int64_t)e * a.m + gr) * a.n + gc;
+          if (a.out_vec)  // n a multiple of 8: the 8 values are all inside, and aligned
+            store_out8(a, o, v);
+          else
+            store_out(a, o, gc, v);
+        }
+      } else {
+        store_pair(a.R0, a.R1, MODE == UPDATE || SPLIT, e * a.r_batch + ((int64_t)(row0 + r) * a.ld + col0 + c) * 2, v);
+      }
+      if (turn)
+#pragma unroll
+        for (int d = 0; d < 2; ++d)
+          *reinterpret_cast<f32x4_t*>(&sc[r * PITCH + c + 4 * d]) =
+              (f32x4_t){v[4 * d], v[4 * d + 1], v[4 * d + 2], v[4 * d + 3]};
+    }
+    wave_lds_fence();
+    if (!turn) return;
+#pragma unroll
+    for (int it = 0; it < W / 16; ++it) {
+      const int c = it * 16 + lane / 4, r = lane % 4 * 8;
+      float v[8];
+#pragma unroll
+      for (int x = 0; x < 8; ++x) v[x] = sc[(r + x) * PITCH + c];
+      if constexpr (MODE == FINAL) {
+        const int gr = col0 + c, gc = row0 + r;  // row and first column of out
+        if (gr < a.m && gc < a.n) {
+          const int64_t o = ((int64_t)e * a.m + gr) * a.n + gc;
+          if (a.out_vec)
+            store_out8(a, o, v);
+          else
+            store_out(a, o, gc, v);
+        }
+      } else {
+        store_pair(a.T0, a.T1, SPLIT, e * a.t_batch + ((int64_t)(col0 + c) * a.ld_t + row0 + r) * 2, v);
+      }
+    }
+    wave_lds_fence();
+  }
+};
+
+template <int MODE, int SIZE, bool SPLIT>
+__global__ __launch_bounds__((64 * Cfg<SIZE, SPLIT>::WM * Cfg<SIZE, SPLIT>::WN)) void product_kernel(const Args a) {
+  using C_ = Cfg<SIZE, SPLIT>;
+  constexpr int RB = C_::RB, NS = C_::NS, B = C_::B, WM = C_::WM, WN = C_::WN, NW = WM * WN;
+  constexpr int WTM = B / WM, WTN = B / WN, MB = WTM / 32, NB = WTN / 32;
+  constexpr int RPI = 1024 / RB;         // rows one wavefront load instruction fills
+  constexpr int INS = B / (NW * RPI);    // load instructions per wavefront and operand array
+  constexpr int ARR = B * RB;            // bytes of an operand array in a stage
+  constexpr int NA = SPLIT ? 4 : 2;      // operand arrays
+  constexpr int STAGE = NA * ARR, NL = NA * INS, CPR = RB / 16;
+  using Epi = Epilogue<MODE, WTN, SPLIT>;
+  constexpr int EPI = NW * 32 * Epi::PITCH * 4;
+  constexpr int SMEM = NS * STAGE > EPI ? NS * STAGE : EPI;
+  constexpr bool SYM = Epi::SYM;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[SMEM];
 
   const int lane = threadIdx.x & 63, wid = uniform_int(threadIdx.x >> 6);
   const int wm = wid / WN, wn = wid % WN;
   const int lr = lane & 31, lh = lane >> 5;
 
-  // ---- workgroup -> (matrix, row tile, column tile); each XCD takes one contiguous range of the tiles
-  const int L = tile::xcd_tile_index(gridDim.x, blockIdx.x);
-  int e, mi, ni;
-  if constexpr (SYM) {
-    // tile t of the upper triangle, column by column: t = ni (ni + 1) / 2 + mi, mi <= ni
-    const int per = a.nt * (a.nt + 1) / 2;
-    e = L / per;
-    const int t = L % per;
-    ni = (int)((sqrtf(8.0f * (float)t + 1.0f) - 1.0f) * 0.5f);
-    while (ni * (ni + 1) / 2 > t) --ni;
-    while ((ni + 1) * (ni + 2) / 2 <= t) ++ni;
-    mi = t - ni * (ni + 1) / 2;
+  // ---- workgroup -> tile (each XCD takes one contiguous range of the whole tiles) and part of its reduction
+  int L = blockIdx.x, part = 0, parts = 1;
+  if (L < a.whole) {
+    L = tile::xcd_tile_index(a.whole, L);
   } else {
-    // groups of 4 row tiles, column tiles next, row tiles fastest: the tiles that an XCD runs at once share operands
-    const int per = a.mt * a.nt;
-    e = L / per;
-    const int t = L % per;
-    const int g = t / (4 * a.nt), r = t % (4 * a.nt);
-    const int gm = min(4, a.mt - g * 4);
-    ni = r / gm;
-    mi = g * 4 + r % gm;
+    parts = a.parts;
+    part = (L - a.whole) % parts;
+    L = a.whole + (L - a.whole) / parts;
   }
-  e = uniform_int(e);
-  const int m0 = uniform_int(mi) * BM, n0 = uniform_int(ni) * BN;
+  const TileAt at = tile_at<MODE>(a, L);
+  const int e = at.e, m0 = at.mi * B, n0 = at.ni * B;
   const int64_t Kb = (int64_t)a.K * 2;
-  const int nk1 = (int)(Kb / RB);            // stages of one pass over the reduction
-  const int nk = SPLIT ? 3 * nk1 : nk1;
+  const int nk_all = (int)(Kb / RB);
+  const int k0 = uniform_int((int)((int64_t)nk_all * part / parts));
+  const int nk = uniform_int((int)((int64_t)nk_all * (part + 1) / parts)) - k0;
 
-  const int64_t moff = e * a.m_batch + m0 * Kb, noff = e * a.n_batch + n0 * Kb;
-  const uint8_t* mb[2] = {uniform_ptr(a.M0 + moff), SPLIT ? uniform_ptr(a.M1 + moff) : nullptr};
-  const uint8_t* nb[2] = {uniform_ptr(a.N0 + noff), SPLIT ? uniform_ptr(a.N1 + noff) : nullptr};
-  uint32_t a_off[A_INS], b_off[B_INS];
-#pragma unroll
-  for (int q = 0; q < A_INS; ++q) {
-    const int r = (wid * A_INS + q) * RPI + lane / CPR;
-    a_off[q] = (uint32_t)(r * Kb + (((lane % CPR) ^ tile::swz<RB>(r)) << 4));
+  const int64_t moff = e * a.m_batch + m0 * Kb + (int64_t)k0 * RB, noff = e * a.n_batch + n0 * Kb + (int64_t)k0 * RB;
+  const uint8_t* base[NA];
+  base[0] = uniform_ptr(a.M0 + moff);
+  base[NA / 2] = uniform_ptr(a.N0 + noff);
+  if constexpr (SPLIT) {
+    base[1] = uniform_ptr(a.M1 + moff);
+    base[3] = uniform_ptr(a.N1 + noff);
   }
+  uint32_t off[INS];
 #pragma unroll
-  for (int q = 0; q < B_INS; ++q) {
-    const int r = (wid * B_INS + q) * RPI + lane / CPR;
-    b_off[q] = (uint32_t)(r * Kb + (((lane % CPR) ^ tile::swz<RB>(r)) << 4));
+  for (int q = 0; q < INS; ++q) {
+    const int r = (wid * INS + q) * RPI + lane / CPR;
+    off[q] = (uint32_t)(r * Kb + (((lane % CPR) ^ tile::swz<RB>(r)) << 4));
   }
   auto load_stage = [&](uint8_t* dst, int kt) {
-    const uint8_t *ab = mb[0], *bb = nb[0];
-    int k = kt;
-    if constexpr (SPLIT) {  // passes: lo hi, hi lo, hi hi (small terms first)
-      if (kt < nk1) {
-        ab = mb[1];
-      } else if (kt < 2 * nk1) {
-        bb = nb[1];
-        k = kt - nk1;
-      } else {
-        k = kt - 2 * nk1;
-      }
+#pragma unroll
+    for (int x = 0; x < NA; ++x) {
+      const uint8_t* p = uniform_ptr(base[x] + (int64_t)kt * RB);
+#pragma unroll
+      for (int q = 0; q < INS; ++q) load_lds16(p, off[q], dst + x * ARR + (wid * INS + q) * 1024);
     }
-    ab = uniform_ptr(ab + (int64_t)k * RB);
-    bb = uniform_ptr(bb + (int64_t)k * RB);
-#pragma unroll
-    for (int q = 0; q < A_INS; ++q) load_lds16(ab, a_off[q], dst + (wid * A_INS + q) * 1024);
-#pragma unroll
-    for (int q = 0; q < B_INS; ++q) load_lds16(bb, b_off[q], dst + BM * RB + (wid * B_INS + q) * 1024);
   };
 
   f32x16_t acc[MB][NB];
@@ -170,6 +368,11 @@ __global__ __launch_bounds__((64 * Cfg<BIG>::WM * Cfg<BIG>::WN)) void product_ke
   const tile::FragOff ao = tile::frag_offsets<RB, RB / 32>(arow[0], lh, 2);
   const tile::FragOff bo = tile::frag_offsets<RB, RB / 32>(brow[0], lh, 2);
 
+  const int row0 = m0 + wm * WTM, col0 = n0 + wn * WTN;
+  typename Epi::Elem el[2];
+  if constexpr (SIZE == 0)
+    if (parts == 1) Epi::load(a, e, row0, col0, el[0]);
+
   // slices 0 .. NS-2 in flight; each iteration waits for its own slice, meets the other wavefronts (the buffer read
   // last iteration is then free), refills it with slice kt + NS - 1 (clamped: loaded, never read) and computes slice kt
 #pragma unroll
@@ -180,137 +383,74 @@ __global__ __launch_bounds__((64 * Cfg<BIG>::WM * Cfg<BIG>::WN)) void product_ke
     __syncthreads();
     load_stage(smem + fb * STAGE, min(kt + NS - 1, nk - 1));
     const uint8_t* As = smem + cb * STAGE;
-    tile::mma_stage_bf16<RB, MB, NB, f16x8_t>(As, As + BM * RB, arow, brow, ao, bo, acc);
+    if constexpr (SPLIT)
+      mma_stage_split<RB, MB, NB>(As, As + 2 * ARR, ARR, ARR, arow, brow, ao, bo, acc);
+    else
+      tile::mma_stage_bf16<RB, MB, NB, f16x8_t>(As, As + ARR, arow, brow, ao, bo, acc);
     cb = cb + 1 == NS ? 0 : cb + 1;
     fb = fb + 1 == NS ? 0 : fb + 1;
   }
-  wait_vmcnt0();
-  __syncthreads();  // no load in flight, no wavefront still reading a stage: the epilogue reuses the buffers
 
-  // ---- epilogue, 32 rows x 64 columns of a wavefront at a time through its own part of LDS, so that every global
-  // access is 16 bytes per lane: by rows for the result (and the elementwise operand), by columns for the transpose.
-  // Accumulator element v of a lane: row (v / 4) * 8 + 4 * (lane / 32) + v % 4, column lane % 32.
-  float* sc = reinterpret_cast<float*>(smem) + wid * 32 * PITCH;
-  const bool mirror = MODE == UPDATE || (SYM && mi != ni);
-  const int64_t rb = e * a.r_batch;
+  // ---- a shared tile: every part leaves its sums in memory, in the accumulators' order (16 bytes per lane side by side),
+  // for the launch that joins them
+  if (parts > 1) {
+    float* mine = a.partial + ((int64_t)(L - a.whole) * parts + part) * (B * B) + wid * (WTM * WTN) + lane * 4;
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          *reinterpret_cast<f32x4_t*>(mine + ((i * NB + j) * 4 + q) * 256) =
+              (f32x4_t){acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+    wait_vmcnt0();  // no load into this workgroup's LDS is outstanding when it ends
+    return;
+  }
+
+  // ---- epilogue, 32 rows at a time; the elementwise operand of a block is loaded while the block before is worked on (the
+  // small tiles' before the product)
+  const bool mirror = MODE == UPDATE || (SYM && at.mi != at.ni);
+  if constexpr (SIZE > 0) Epi::load(a, at.e, row0, col0, el[0]);
+  wait_vmcnt0();
+  __syncthreads();  // no load into LDS in flight, no wavefront still reading a stage: the epilogue reuses the buffers
+  float* sc = reinterpret_cast<float*>(smem) + wid * 32 * Epi::PITCH;
 #pragma unroll
   for (int i = 0; i < MB; ++i) {
+    if (i + 1 < MB) Epi::load(a, at.e, row0 + (i + 1) * 32, col0, el[(i + 1) & 1]);
+    Epi::run(a, at.e, row0 + i * 32, col0, mirror, acc[i], el[i & 1], sc);
+  }
+}
+
+// The shared tiles: adds the parts' sums in the order of the parts and finishes the tile.  One wavefront per 32 x WTN block.
+template <int MODE, int SIZE, bool SPLIT>
+__global__ __launch_bounds__(256) void join_kernel(const Args a) {
+  using C_ = Cfg<SIZE, SPLIT>;
+  constexpr int B = C_::B, WTM = B / C_::WM, WTN = B / C_::WN, MB = WTM / 32, NB = WTN / 32;
+  constexpr int BLOCKS = C_::WM * C_::WN * MB;  // of a tile
+  using Epi = Epilogue<MODE, WTN, SPLIT>;
+  __shared__ float smem[4 * 32 * Epi::PITCH];
+  const int lane = threadIdx.x & 63, w4 = uniform_int(threadIdx.x >> 6);
+  const int blk = blockIdx.x * 4 + w4, rest = blk / BLOCKS, wid = blk % BLOCKS / MB, i = blk % MB;
+  const TileAt at = tile_at<MODE>(a, a.whole + rest);
+  const int row0 = at.mi * B + wid / C_::WN * WTM + i * 32, col0 = at.ni * B + wid % C_::WN * WTN;
+  typename Epi::Elem el;
+  Epi::load(a, at.e, row0, col0, el);
+  const float* p = a.partial + (int64_t)rest * a.parts * (B * B) + wid * (WTM * WTN) + i * NB * 1024 + lane * 4;
+  f32x16_t acc[NB];
+#pragma unroll
+  for (int j = 0; j < NB; ++j)
+#pragma unroll
+    for (int v = 0; v < 16; ++v) acc[j][v] = 0.0f;
+  for (int x = 0; x < a.parts; ++x, p += B * B)
 #pragma unroll
     for (int j = 0; j < NB; ++j)
 #pragma unroll
-      for (int v = 0; v < 16; ++v)
-        sc[((v >> 2) * 8 + 4 * lh + (v & 3)) * PITCH + j * 32 + lr] = acc[i][j][v];
-    wave_lds_fence();
-    const int row0 = m0 + wm * WTM + i * 32, col0 = n0 + wn * WTN;
+      for (int q = 0; q < 4; ++q) {
+        const f32x4_t t = *reinterpret_cast<const f32x4_t*>(p + (j * 4 + q) * 256);
 #pragma unroll
-    for (int it = 0; it < 4; ++it) {
-      const int r = it * 8 + lane / 8, c = lane % 8 * 8;
-      float v[8];
-#pragma unroll
-      for (int d = 0; d < 2; ++d) {
-        const f32x4_t q = *reinterpret_cast<const f32x4_t*>(&sc[r * PITCH + c + 4 * d]);
-#pragma unroll
-        for (int x = 0; x < 4; ++x) v[4 * d + x] = a.beta * q[x];
+        for (int v = 0; v < 4; ++v) acc[j][4 * q + v] += t[v];
       }
-      const int64_t at = rb + ((int64_t)(row0 + r) * a.ld + col0 + c) * 2;
-      if constexpr (MODE != GRAM) {
-        const f16x8_t h = *reinterpret_cast<const f16x8_t*>(a.E0 + at);
-        f16x8_t l;
-        if constexpr (MODE != POLY || SPLIT) l = *reinterpret_cast<const f16x8_t*>(a.E1 + at);
-#pragma unroll
-        for (int x = 0; x < 8; ++x) {
-          float ev = (float)h[x];
-          if constexpr (MODE != POLY || SPLIT) ev += (float)l[x];
-          v[x] = __builtin_fmaf(a.alpha, ev, v[x]);
-        }
-      }
-      if constexpr (MODE == FINAL) {
-        if (!a.flip) {
-          const int gr = row0 + r, gc = col0 + c;
-          if (gr < a.m && gc < a.n) {
-            const int64_t o = ((int64_t)e * a.m + gr) * a.n + gc;
-            if (a.out_vec) {  // n a multiple of 8: the 8 values are all inside, and aligned
-              if (a.out_bf16) {
-                i32x4_t w;
-#pragma unroll
-                for (int d = 0; d < 4; ++d)
-                  w[d] = (int)((uint32_t)f32_to_bf16_bits(v[2 * d]) | ((uint32_t)f32_to_bf16_bits(v[2 * d + 1]) << 16));
-                *reinterpret_cast<i32x4_t*>(a.out + o * 2) = w;
-              } else {
-#pragma unroll
-                for (int d = 0; d < 2; ++d)
-                  *reinterpret_cast<f32x4_t*>(a.out + o * 4 + 16 * d) =
-                      (f32x4_t){v[4 * d], v[4 * d + 1], v[4 * d + 2], v[4 * d + 3]};
-              }
-            } else {
-#pragma unroll
-              for (int x = 0; x < 8; ++x)
-                if (gc + x < a.n) {
-                  if (a.out_bf16)
-                    reinterpret_cast<uint16_t*>(a.out)[o + x] = f32_to_bf16_bits(v[x]);
-                  else
-                    reinterpret_cast<float*>(a.out)[o + x] = v[x];
-                }
-            }
-          }
-        }
-      } else {
-        f16x8_t h, l;
-#pragma unroll
-        for (int x = 0; x < 8; ++x) {
-          _Float16 hi, lo;
-          split16(v[x], hi, lo);
-          h[x] = hi;
-          l[x] = lo;
-        }
-        *reinterpret_cast<f16x8_t*>(a.R0 + at) = h;
-        if constexpr (MODE == UPDATE || SPLIT) *reinterpret_cast<f16x8_t*>(a.R1 + at) = l;
-      }
-      if (MODE != FINAL ? mirror : a.flip) {
-#pragma unroll
-        for (int d = 0; d < 2; ++d)
-          *reinterpret_cast<f32x4_t*>(&sc[r * PITCH + c + 4 * d]) =
-              (f32x4_t){v[4 * d], v[4 * d + 1], v[4 * d + 2], v[4 * d + 3]};
-      }
-    }
-    wave_lds_fence();
-    if (MODE != FINAL ? mirror : a.flip) {
-#pragma unroll
-      for (int it = 0; it < 4; ++it) {
-        const int c = it * 16 + lane / 4, r = lane % 4 * 8;
-        float v[8];
-#pragma unroll
-        for (int x = 0; x < 8; ++x) v[x] = sc[(r + x) * PITCH + c];
-        if constexpr (MODE == FINAL) {
-          const int gr = col0 + c, gc = row0 + r;  // row and first column of out
-          if (gr < a.m) {
-            const int64_t o = ((int64_t)e * a.m + gr) * a.n + gc;
-#pragma unroll
-            for (int x = 0; x < 8; ++x)
-              if (gc + x < a.n) {
-                if (a.out_bf16)
-                  reinterpret_cast<uint16_t*>(a.out)[o + x] = f32_to_bf16_bits(v[x]);
-                else
-                  reinterpret_cast<float*>(a.out)[o + x] = v[x];
-              }
-          }
-        } else {
-          f16x8_t h, l;
-#pragma unroll
-          for (int x = 0; x < 8; ++x) {
-            _Float16 hi, lo;
-            split16(v[x], hi, lo);
-            h[x] = hi;
-            l[x] = lo;
-          }
-          const int64_t at = e * a.t_batch + ((int64_t)(col0 + c) * a.ld_t + row0 + r) * 2;
-          *reinterpret_cast<f16x8_t*>(a.T0 + at) = h;
-          if constexpr (SPLIT) *reinterpret_cast<f16x8_t*>(a.T1 + at) = l;
-        }
-      }
-      wave_lds_fence();
-    }
-  }
+  Epi::run(a, at.e, row0, col0, MODE == UPDATE || (Epi::SYM && at.mi != at.ni), acc, el, smem + w4 * 32 * Epi::PITCH);
 }
 
 MOE_DEV float load_g(const uint8_t* g, bool bf16, int64_t i) {
@@ -392,12 +532,63 @@ __global__ __launch_bounds__(256) void prepare_kernel(const PrepArgs a) {
   }
 }
 
+constexpr int CUS = 256, MOST_PARTS = 8;
+
+// How one product is laid over the GPU: the tile size (index of TILE), the tiles that are one workgroup each, and the
+// parts of each of the others.
+struct Shape {
+  int size, whole, parts, rest;
+};
+
+// Microseconds of a product, to choose by: a launch of its own, then for every 256 tiles (one per compute unit; two smaller
+// tiles that share one take as long as one after the other) the reduction and the epilogue.  Measured on kernels of 24 to
+// 8192 tiles, K = 512 to 14336; one 256 x 256 tile holds 16 of 64 x 64, so per value the sizes cost 25 : 37 : 67.
+//                               64 x 64        128 x 128      256 x 256
+constexpr double PER_K[2][3] = {{4.2e-3, 9.2e-3, 25e-3}, {8.5e-3, 27e-3, 72e-3}};  // [SPLIT]
+constexpr double EPI_SYM[2][3] = {{1.0, 4.0, 10.0}, {1.5, 6.0, 15.0}};
+constexpr double EPI_UPDATE[2][3] = {{1.0, 5.0, 33.0}, {1.5, 7.0, 50.0}};
+constexpr double LAUNCH_US = 4.5, BYTES_PER_US = 4e6;
+
+static Shape shape(int64_t batch, int rows, int cols, int K, bool sym, int most_size, bool split) {
+  Shape best{};
+  double best_us = 1e30;
+  for (int size = 0; size <= most_size; ++size) {
+    const int64_t nt = cols / TILE[size];
+    const int64_t tiles = (sym ? nt * (nt + 1) / 2 : (int64_t)(rows / TILE[size]) * nt) * batch;
+    const double epi = sym ? EPI_SYM[split][size] : EPI_UPDATE[split][size], red = K * PER_K[split][size];
+    const int64_t full = tiles / CUS;
+    const int rest = (int)(tiles % CUS);
+    const int stages = K / (size == 1 || (size == 2 && split) ? 32 : 64);
+    // the tiles of the last, partial round: whole, or each shared by `parts` workgroups and joined by another launch
+    int parts = rest > 0 ? CUS / rest : 1;
+    if (parts > MOST_PARTS) parts = MOST_PARTS;
+    if (parts > stages / 4) parts = stages / 4;
+    for (int x = 1; x <= (parts < 1 ? 1 : parts); ++x) {
+      const double bytes = 2.0 * rest * x * TILE[size] * TILE[size] * sizeof(float);
+      const double us = LAUNCH_US + full * (red + epi) +
+                        (rest == 0 ? 0.0 : x == 1 ? red + epi : red / x + LAUNCH_US + bytes / BYTES_PER_US);
+      if (us < best_us) {
+        best_us = us;
+        best.size = size;
+        best.parts = x;
+        best.rest = x > 1 ? rest : 0;
+        best.whole = (int)(tiles - best.rest);
+      }
+    }
+  }
+  return best;
+}
+static size_t partial_bytes(const Shape& z) {
+  return (size_t)z.rest * z.parts * TILE[z.size] * TILE[z.size] * sizeof(float);
+}
+
 struct Plan {
   int p, q, P, Q;
-  bool flip, big;
+  bool flip;
   int chunks;
+  Shape gram, poly, update;
   size_t x_bytes, a_bytes;  // one fp16 array of the whole batch
-  size_t part_bytes, total;
+  size_t part_bytes, partial, total;
 };
 
 static size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
@@ -407,32 +598,51 @@ static Plan plan(int64_t batch, int m, int n, bool split) {
   z.flip = m > n;
   z.p = z.flip ? n : m;
   z.q = z.flip ? m : n;
-  // 256 x 256 tiles where the update's tiles fill the 256 compute units, 128 x 128 otherwise
-  z.big = (int64_t)((z.p + 255) / 256) * ((z.q + 255) / 256) * batch >= 256;
-  const int tl = z.big ? 256 : 128;
+  // the largest tile that the products choose from sets the padding
+  auto tiles_of = [&](int t) { return (int64_t)((z.p + t - 1) / t) * ((z.q + t - 1) / t) * batch; };
+  const int most = tiles_of(256) >= CUS / 2 ? 2 : tiles_of(128) >= CUS / 2 ? 1 : 0;
+  const int tl = TILE[most];
   z.P = (z.p + tl - 1) / tl * tl;
   z.Q = (z.q + tl - 1) / tl * tl;
+  z.gram = shape(batch, z.P, z.P, z.Q, true, most, split);
+  z.poly = shape(batch, z.P, z.P, z.P, true, most, split);
+  z.update = shape(batch, z.P, z.Q, z.P, false, most, split);
   const int64_t count = (int64_t)m * n;
   z.chunks = (int)(count / 4096 < 1 ? 1 : count / 4096 > 256 ? 256 : count / 4096);
   z.x_bytes = (size_t)batch * z.P * z.Q * 2;
   z.a_bytes = (size_t)batch * z.P * z.P * 2;
   z.part_bytes = up256((size_t)batch * z.chunks * sizeof(double));
-  z.total = z.part_bytes + (split ? 6 : 4) * z.x_bytes + (split ? 4 : 2) * z.a_bytes;
+  for (const Shape* t : {&z.gram, &z.poly, &z.update})
+    if (partial_bytes(*t) > z.partial) z.partial = partial_bytes(*t);
+  z.total = z.part_bytes + z.partial + (split ? 6 : 4) * z.x_bytes +
+            (split ? 4 : 2) * z.a_bytes;
   return z;
 }
 
+template <int MODE, int SIZE, bool SPLIT>
+static void launch_sized(const Args& a, const Shape& z, hipStream_t s) {
+  using C_ = Cfg<SIZE, SPLIT>;
+  hipLaunchKernelGGL((product_kernel<MODE, SIZE, SPLIT>), dim3((unsigned)(z.whole + z.rest * z.parts)),
+                     dim3(64 * C_::WM * C_::WN), 0, s, a);
+  // 32-row blocks of a tile: SIZE 0: 2 x 2 x 1, 1: 2 x 2 x 2, 2: 2 x 4 x 4; four to a workgroup
+  constexpr int GROUPS = C_::WM * C_::WN * (C_::B / C_::WM / 32) / 4;
+  if (z.rest > 0)
+    hipLaunchKernelGGL((join_kernel<MODE, SIZE, SPLIT>), dim3((unsigned)(z.rest * GROUPS)), dim3(256), 0, s, a);
+}
+
 template <int MODE, bool SPLIT>
-static void launch_product(const Args& a0, bool big, int rows, int cols, int64_t batch, hipStream_t s) {
+static void launch_product(const Args& a0, const Shape& z, int rows, int cols, hipStream_t s) {
   Args a = a0;
-  const int tl = big ? 256 : 128;
-  a.mt = rows / tl;
-  a.nt = cols / tl;
-  const int64_t per = MODE == GRAM || MODE == POLY ? (int64_t)a.nt * (a.nt + 1) / 2 : (int64_t)a.mt * a.nt;
-  const dim3 grid((unsigned)(per * batch));
-  if (big)
-    hipLaunchKernelGGL((product_kernel<MODE, 1, SPLIT>), grid, dim3(512), 0, s, a);
+  a.mt = rows / TILE[z.size];
+  a.nt = cols / TILE[z.size];
+  a.whole = z.whole;
+  a.parts = z.parts;
+  if (z.size == 2)
+    launch_sized<MODE, 2, SPLIT>(a, z, s);
+  else if (z.size == 1)
+    launch_sized<MODE, 1, SPLIT>(a, z, s);
   else
-    hipLaunchKernelGGL((product_kernel<MODE, 0, SPLIT>), grid, dim3(256), 0, s, a);
+    launch_sized<MODE, 0, SPLIT>(a, z, s);
 }
 
 template <bool SPLIT>
@@ -445,6 +655,7 @@ static void run(const OrthLaunch& p, hipStream_t s) {
     return r;
   };
   double* part = reinterpret_cast<double*>(take(z.part_bytes));
+  float* partial = reinterpret_cast<float*>(take(z.partial));
   uint8_t *x0 = take(z.x_bytes), *x1 = take(z.x_bytes);
   uint8_t *t0[2] = {take(z.x_bytes), take(z.x_bytes)}, *t1[2] = {nullptr, nullptr};
   uint8_t *a0 = take(z.a_bytes), *b0 = take(z.a_bytes), *a1 = nullptr, *b1 = nullptr;
@@ -480,6 +691,7 @@ static void run(const OrthLaunch& p, hipStream_t s) {
   for (int k = 0; k < p.steps; ++k) {
     const int cur = k & 1, nxt = cur ^ 1;
     Args q{};
+    q.partial = partial;
     q.M0 = q.N0 = x0;  // A = X X^T
     q.M1 = q.N1 = x1;
     q.m_batch = q.n_batch = xb;
@@ -489,7 +701,7 @@ static void run(const OrthLaunch& p, hipStream_t s) {
     q.ld = q.ld_t = z.P;
     q.r_batch = q.t_batch = ab;
     q.beta = 1.0f / S;
-    launch_product<GRAM, SPLIT>(q, z.big, z.P, z.P, p.batch, s);
+    launch_product<GRAM, SPLIT>(q, z.gram, z.P, z.P, s);
     q.M0 = q.N0 = q.E0 = a0;  // B = b A + c A A
     q.M1 = q.N1 = q.E1 = a1;
     q.m_batch = q.n_batch = ab;
@@ -498,7 +710,7 @@ static void run(const OrthLaunch& p, hipStream_t s) {
     q.R1 = q.T1 = b1;
     q.alpha = p.b;
     q.beta = p.c / S;
-    launch_product<POLY, SPLIT>(q, z.big, z.P, z.P, p.batch, s);
+    launch_product<POLY, SPLIT>(q, z.poly, z.P, z.P, s);
     q.M0 = b0;  // X <- a X + B X
     q.M1 = b1;
     q.N0 = t0[cur];
@@ -514,7 +726,7 @@ static void run(const OrthLaunch& p, hipStream_t s) {
     q.alpha = p.a;
     q.beta = 1.0f / S;
     if (k + 1 < p.steps) {
-      launch_product<UPDATE, SPLIT>(q, z.big, z.P, z.Q, p.batch, s);
+      launch_product<UPDATE, SPLIT>(q, z.update, z.P, z.Q, s);
     } else {
       q.alpha = p.a * (p.scale / S);
       q.beta = p.scale / S / S;
@@ -524,7 +736,7 @@ static void run(const OrthLaunch& p, hipStream_t s) {
       q.flip = z.flip;
       q.out_bf16 = p.out_bf16;
       q.out_vec = p.n % 8 == 0 && (uintptr_t)p.out % 16 == 0;
-      launch_product<FINAL, SPLIT>(q, z.big, z.P, z.Q, p.batch, s);
+      launch_product<FINAL, SPLIT>(q, z.update, z.P, z.Q, s);
     }
   }
 }
