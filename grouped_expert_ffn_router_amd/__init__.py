@@ -134,7 +134,7 @@ def _ptr(t):
 
 def _stream(stream):
     if stream is None:
-        stream = torch.cuda.current_stream()
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
@@ -457,43 +457,53 @@ def moe_combine_slots(y_slot, topk_idx, e_lo=0, E_local=None, out_dtype=torch.bf
     return out
 
 
+_CURRENT = contextlib.nullcontext()
+
+
 def _on_device(fn, dev, stream):
     """Context of a call on tensors of device ``dev``: kernels are launched with that device current."""
     if dev.type != "cuda":
         raise ValueError(f"{fn}: tensors must be on the GPU (got {dev})")
     if isinstance(stream, torch.cuda.Stream) and stream.device != dev:
         raise ValueError(f"{fn}: the stream is on {stream.device}, the tensors on {dev}")
-    return contextlib.nullcontext() if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+    return _CURRENT if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
 
 
-def _tensor(fn, name, t, shape, dtypes, dev, contiguous=True):
-    """Checks one tensor argument against what the C call assumes of its pointer; returns it."""
+def _tensor(fn, name, t, shape, dtypes, index):
+    """Checks one contiguous tensor argument on GPU ``index`` (-1: the CPU) against what the C call assumes of its
+    pointer; returns the pointer."""
     if t.shape != shape:
         raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, not {tuple(shape)}")
     if t.dtype not in dtypes:
         raise ValueError(f"{fn}: {name} has dtype {t.dtype}, not {' or '.join(map(str, dtypes))}")
-    if t.device != dev:
-        raise ValueError(f"{fn}: {name} is on {t.device}, not {dev}")
-    if contiguous and not t.is_contiguous():
+    if t.get_device() != index:
+        raise ValueError(f"{fn}: {name} is on {t.device}, the rows or matrices are not")
+    if not t.is_contiguous():
         raise ValueError(f"{fn}: {name} must be contiguous")
-    return t
+    return t.data_ptr()
 
 
-def _rows(fn, name, t, shape, dtype, dev):
-    """Checks rows whose values are contiguous and whose stride is free; returns the stride in elements."""
-    _tensor(fn, name, t, shape, (dtype,), dev, contiguous=False)
+def _rows(fn, name, t, shape, dtype, index):
+    """Checks rows whose values are contiguous and whose stride is free; returns the pointer and the stride in elements."""
+    if t.is_contiguous():
+        return _tensor(fn, name, t, shape, (dtype,), index), shape[1]
+    if t.shape != shape:
+        raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{fn}: {name} has dtype {t.dtype}, not {dtype}")
+    if t.get_device() != index:
+        raise ValueError(f"{fn}: {name} is on {t.device}, the rows are not")
     T, H = shape
     if H > 1 and t.stride(1) != 1:
         raise ValueError(f"{fn}: {name}'s rows must be contiguous")
-    if T <= 1:
-        return H
-    if t.stride(0) < H:
+    if T > 1 and t.stride(0) < H:
         raise ValueError(f"{fn}: {name}'s rows overlap")
-    return t.stride(0)
+    return t.data_ptr(), t.stride(0) if T > 1 else H
 
 
 _ROW_TYPES = (torch.float32, torch.bfloat16)
 _FP8_TYPES = (torch.uint8, torch.float8_e4m3fn)
+_F32 = (torch.float32,)
 
 
 @dataclasses.dataclass
@@ -512,8 +522,8 @@ def _norm_args(fn, x, weight, kind):
         raise ValueError(f"{fn}: rows must be [T, H] (got {tuple(x.shape)})")
     if x.dtype not in _ROW_TYPES:
         raise ValueError(f"{fn}: rows must be float32 or bfloat16 (got {x.dtype})")
-    _tensor(fn, "weight", weight, (x.shape[1],), _ROW_TYPES, x.device)
-    return x.shape
+    index = x.get_device()
+    return x.shape, index, _tensor(fn, "weight", weight, x.shape[1:], _ROW_TYPES, index)
 
 
 def moe_norm(x, weight, bias=None, residual=None, kind="layer", eps=1e-5, out_dtype=None, y=None, y_scales=None,
@@ -524,48 +534,45 @@ def moe_norm(x, weight, bias=None, residual=None, kind="layer", eps=1e-5, out_dt
     out_dtype: x's (default), or torch.float8_e4m3fn / torch.uint8: e4m3 codes with y_scales [T, H/128], as
     moe_dispatch_permute takes them.  ``sum`` may be x or residual themselves."""
     fn = "moe_norm"
-    T, H = _norm_args(fn, x, weight, kind)
-    dev = x.device
-    ldx = _rows(fn, "x", x, (T, H), x.dtype, dev)
-    ldr = 0 if residual is None else _rows(fn, "residual", residual, (T, H), x.dtype, dev)
-    if bias is not None:
-        _tensor(fn, "bias", bias, (H,), (weight.dtype,), dev)
+    shape, index, w_ptr = _norm_args(fn, x, weight, kind)
+    T, H = shape
+    dt = x.dtype
+    x_ptr, ldx = _rows(fn, "x", x, shape, dt, index)
+    r_ptr, ldr = (None, 0) if residual is None else _rows(fn, "residual", residual, shape, dt, index)
+    b_ptr = None if bias is None else _tensor(fn, "bias", bias, weight.shape, (weight.dtype,), index)
     if y is not None and out_dtype is not None and y.dtype != out_dtype:
         raise ValueError(f"{fn}: y has dtype {y.dtype}, not {out_dtype}")
-    yt = y.dtype if y is not None else out_dtype or x.dtype
+    yt = y.dtype if y is not None else out_dtype or dt
     fp8 = yt in _FP8_TYPES
-    if not fp8 and yt != x.dtype:
+    if not fp8 and yt != dt:
         raise NotImplementedError(f"{fn}: the output is the rows' dtype or e4m3 codes, not {yt}")
     if fp8 and H % 128:
         raise ValueError(f"{fn}: e4m3 rows need H = {H} to be a multiple of 128")
     layer = kind == "layer"
-    with _on_device(fn, dev, stream):
+    with _on_device(fn, x.device, stream):
         if (y is None or rstd is None or (fp8 and y_scales is None) or (layer and mean is None)
                 or (residual is not None and sum is None)):
+            dev = x.device
             with _alloc_on(stream):
                 if y is None:
                     y = torch.empty((T, H), dtype=yt, device=dev)
                 if fp8 and y_scales is None:
                     y_scales = torch.empty((T, H // 128), dtype=torch.float32, device=dev)
                 if residual is not None and sum is None:
-                    sum = torch.empty((T, H), dtype=x.dtype, device=dev)
+                    sum = torch.empty((T, H), dtype=dt, device=dev)
                 if layer and mean is None:
                     mean = torch.empty(T, dtype=torch.float32, device=dev)
                 if rstd is None:
                     rstd = torch.empty(T, dtype=torch.float32, device=dev)
-        _tensor(fn, "y", y, (T, H), (yt,), dev)
-        _tensor(fn, "rstd", rstd, (T,), (torch.float32,), dev)
-        if fp8:
-            _tensor(fn, "y_scales", y_scales, (T, H // 128), (torch.float32,), dev)
-        if layer:
-            _tensor(fn, "mean", mean, (T,), (torch.float32,), dev)
-        if residual is not None:
-            _tensor(fn, "sum", sum, (T, H), (x.dtype,), dev)
-        _check(lib.moe_norm(_ptr(x), ldx, _ptr(residual), ldr, dtype_code(x.dtype), T, H, NORM_KINDS[kind],
-                            _ptr(weight), _ptr(bias), dtype_code(weight.dtype), eps,
-                            _ptr(sum) if residual is not None else None, _ptr(y), _ptr(y_scales) if fp8 else None,
-                            dtype_code(yt), _ptr(mean) if layer else None, _ptr(rstd), _stream(stream)), fn)
-    return Norm(y, y_scales if fp8 else None, sum if residual is not None else x, mean if layer else None, rstd)
+        y_ptr = _tensor(fn, "y", y, shape, (yt,), index)
+        rstd_ptr = _tensor(fn, "rstd", rstd, shape[:1], _F32, index)
+        ys_ptr = _tensor(fn, "y_scales", y_scales, (T, H // 128), _F32, index) if fp8 else None
+        mean_ptr = _tensor(fn, "mean", mean, shape[:1], _F32, index) if layer else None
+        sum_ptr = None if residual is None else _tensor(fn, "sum", sum, shape, (dt,), index)
+        _check(lib.moe_norm(x_ptr, ldx, r_ptr, ldr, dtype_code(dt), T, H, NORM_KINDS[kind], w_ptr, b_ptr,
+                            dtype_code(weight.dtype), eps, sum_ptr, y_ptr, ys_ptr, dtype_code(yt), mean_ptr, rstd_ptr,
+                            _stream(stream)), fn)
+    return Norm(y, y_scales if fp8 else None, x if residual is None else sum, mean if layer else None, rstd)
 
 
 def moe_norm_backward_workspace_bytes(T, H) -> int:
@@ -577,23 +584,25 @@ def moe_norm_backward(dy, rows, weight, mean, rstd, kind="layer", dsum=None, wan
     """Gradients of moe_norm for dy = dL/dy: dict(dx [T, H], dweight [H] fp32, dbias [H] fp32 or None).
 
     rows: what was normalised (Norm.sum); dx is its gradient, with dsum (the gradient that reaches the rows by the
-    residual stream) added.  dx may be dy or dsum themselves (out["dx"]).  want_bias: default, for kind "layer" only."""
+    residual stream) added.  dx may be dy or dsum themselves (out["dx"]).  want_bias: default, for kind "layer" only
+    (with ``out``: where out["dbias"] is given)."""
     fn = "moe_norm_backward"
-    T, H = _norm_args(fn, rows, weight, kind)
-    dev, dt = rows.device, rows.dtype
+    shape, index, w_ptr = _norm_args(fn, rows, weight, kind)
+    T, H = shape
+    dt = rows.dtype
     layer = kind == "layer"
     if want_bias is None:
         want_bias = layer if out is None else out.get("dbias") is not None
-    ld_s = _rows(fn, "rows", rows, (T, H), dt, dev)
-    ld_dy = _rows(fn, "dy", dy, (T, H), dt, dev)
-    ld_ds = 0 if dsum is None else _rows(fn, "dsum", dsum, (T, H), dt, dev)
-    if layer:
-        if mean is None:
-            raise ValueError(f"{fn}: kind 'layer' needs the rows' means")
-        _tensor(fn, "mean", mean, (T,), (torch.float32,), dev)
-    _tensor(fn, "rstd", rstd, (T,), (torch.float32,), dev)
-    with _on_device(fn, dev, stream):
+    s_ptr, ld_s = _rows(fn, "rows", rows, shape, dt, index)
+    dy_ptr, ld_dy = _rows(fn, "dy", dy, shape, dt, index)
+    ds_ptr, ld_ds = (None, 0) if dsum is None else _rows(fn, "dsum", dsum, shape, dt, index)
+    if layer and mean is None:
+        raise ValueError(f"{fn}: kind 'layer' needs the rows' means")
+    mean_ptr = _tensor(fn, "mean", mean, shape[:1], _F32, index) if layer else None
+    rstd_ptr = _tensor(fn, "rstd", rstd, shape[:1], _F32, index)
+    with _on_device(fn, rows.device, stream):
         if out is None or workspace is None:
+            dev = rows.device
             with _alloc_on(stream):
                 if out is None:
                     out = dict(dx=torch.empty((T, H), dtype=dt, device=dev),
@@ -601,18 +610,14 @@ def moe_norm_backward(dy, rows, weight, mean, rstd, kind="layer", dsum=None, wan
                                dbias=torch.empty(H, dtype=torch.float32, device=dev) if want_bias else None)
                 if workspace is None:
                     workspace = torch.empty(moe_norm_backward_workspace_bytes(T, H), dtype=torch.uint8, device=dev)
-        _tensor(fn, "dx", out["dx"], (T, H), (dt,), dev)
-        _tensor(fn, "dweight", out["dweight"], (H,), (torch.float32,), dev)
-        if want_bias:
-            if out.get("dbias") is None:
-                raise ValueError(f"{fn}: want_bias needs out['dbias']")
-            _tensor(fn, "dbias", out["dbias"], (H,), (torch.float32,), dev)
-        _workspace(fn, workspace, dev)
-        _check(lib.moe_norm_backward(_ptr(dy), ld_dy, _ptr(rows), ld_s, _ptr(dsum), ld_ds, dtype_code(dt), T, H,
-                                     NORM_KINDS[kind], _ptr(weight), dtype_code(weight.dtype),
-                                     _ptr(mean) if layer else None, _ptr(rstd), _ptr(out["dx"]), _ptr(out["dweight"]),
-                                     _ptr(out["dbias"]) if want_bias else None, _ptr(workspace), _nbytes(workspace),
-                                     _stream(stream)), fn)
+        dx_ptr = _tensor(fn, "dx", out["dx"], shape, (dt,), index)
+        dw_ptr = _tensor(fn, "dweight", out["dweight"], shape[1:], _F32, index)
+        if want_bias and out.get("dbias") is None:
+            raise ValueError(f"{fn}: want_bias needs out['dbias']")
+        db_ptr = _tensor(fn, "dbias", out["dbias"], shape[1:], _F32, index) if want_bias else None
+        _check(lib.moe_norm_backward(dy_ptr, ld_dy, s_ptr, ld_s, ds_ptr, ld_ds, dtype_code(dt), T, H, NORM_KINDS[kind],
+                                     w_ptr, dtype_code(weight.dtype), mean_ptr, rstd_ptr, dx_ptr, dw_ptr, db_ptr,
+                                     *_workspace(fn, workspace, index), _stream(stream)), fn)
     return out
 
 
@@ -620,9 +625,11 @@ def _nbytes(t) -> int:
     return t.numel() * t.element_size()
 
 
-def _workspace(fn, t, dev):
-    if t.device != dev or not t.is_contiguous():
-        raise ValueError(f"{fn}: the workspace must be contiguous and on {dev}")
+def _workspace(fn, t, index):
+    """Pointer and size of a workspace tensor."""
+    if t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{fn}: the workspace must be contiguous and on the GPU of the other tensors")
+    return t.data_ptr(), _nbytes(t)
 
 
 # singular values 0.003 .. 1 come out between 0.68 and 1.21 after five steps
@@ -643,9 +650,9 @@ def moe_orthogonalize(g, steps=5, coeffs=ORTHOGONALIZE_COEFFS, eps=1e-7, scale=1
     fn = "moe_orthogonalize"
     if g.dim() not in (2, 3):
         raise ValueError(f"{fn}: g must be [B, m, n] or [m, n] (got {tuple(g.shape)})")
-    dev = g.device
+    index = g.get_device()
     B, m, n = g.shape if g.dim() == 3 else (1, *g.shape)
-    _tensor(fn, "g", g, g.shape, _ROW_TYPES, dev)
+    g_ptr = _tensor(fn, "g", g, g.shape, _ROW_TYPES, index)
     if len(coeffs) != 3:
         raise ValueError(f"{fn}: coeffs are three numbers")
     if out is not None and out_dtype is not None and out.dtype != out_dtype:
@@ -653,22 +660,19 @@ def moe_orthogonalize(g, steps=5, coeffs=ORTHOGONALIZE_COEFFS, eps=1e-7, scale=1
     ot = out.dtype if out is not None else out_dtype or torch.bfloat16
     if ot not in _ROW_TYPES:
         raise ValueError(f"{fn}: the output must be float32 or bfloat16 (got {ot})")
-    with _on_device(fn, dev, stream):
+    with _on_device(fn, g.device, stream):
         if out is None or workspace is None:
             with _alloc_on(stream):
                 if out is None:
-                    out = torch.empty(g.shape, dtype=ot, device=dev)
+                    out = torch.empty(g.shape, dtype=ot, device=g.device)
                 if workspace is None:
                     workspace = torch.empty(moe_orthogonalize_workspace_bytes(B, m, n, ot), dtype=torch.uint8,
-                                            device=dev)
-        _tensor(fn, "out", out, g.shape, (ot,), dev)
-        if g.numel() and out.untyped_storage().data_ptr() == g.untyped_storage().data_ptr():
-            a0, b0 = g.data_ptr(), out.data_ptr()
-            if a0 < b0 + _nbytes(out) and b0 < a0 + _nbytes(g):
-                raise ValueError(f"{fn}: out must not overlap g")
-        _workspace(fn, workspace, dev)
-        _check(lib.moe_orthogonalize(_ptr(g), dtype_code(g.dtype), B, m, n, steps, *coeffs, eps, scale, _ptr(out),
-                                     dtype_code(ot), _ptr(workspace), _nbytes(workspace), _stream(stream)), fn)
+                                            device=g.device)
+        out_ptr = _tensor(fn, "out", out, g.shape, (ot,), index)
+        if g_ptr < out_ptr + _nbytes(out) and out_ptr < g_ptr + _nbytes(g):
+            raise ValueError(f"{fn}: out must not overlap g")
+        _check(lib.moe_orthogonalize(g_ptr, dtype_code(g.dtype), B, m, n, steps, *coeffs, eps, scale, out_ptr,
+                                     dtype_code(ot), *_workspace(fn, workspace, index), _stream(stream)), fn)
     return out
 
 

@@ -689,8 +689,6 @@ moe_status moe_norm(const void* x, int64_t ldx, const void* residual, int64_t ld
   p.y_scales = y_scales;
   p.mean = mean;
   p.rstd = rstd;
-  if (fp8 && !norm_vector_ok(p))
-    FAIL(MOE_ERR_INVALID_ARG, "%s: FP8_E4M3 needs 16-byte aligned rows and parameters", fn);
   launch_norm(p, (hipStream_t)stream);
   return launch_status(fn);
 }

@@ -99,7 +99,6 @@ struct NormLaunch {
   float* part;  // workspace: [2][norm_backward_groups][H]
 };
 int norm_backward_groups(int64_t T, int H);
-bool norm_vector_ok(const NormLaunch& p);  // whether every operand takes 16-byte accesses
 void launch_norm(const NormLaunch& p, hipStream_t s);
 void launch_norm_backward(const NormLaunch& p, hipStream_t s);
 

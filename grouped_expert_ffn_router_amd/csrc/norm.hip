@@ -9,8 +9,8 @@
 // writes ds once; a row stays in registers between its statistics and its result.  TPR threads share a row, 16
 // columns each (TPR = 16 .. 1024 by powers of two; rows above 16384 columns take 64 per thread), so a thread has two
 // to four 16-byte loads of each operand in flight and the two sums of a row cost one or two exchanges: in a wavefront
-// by lane shuffles, across wavefronts through LDS.  Rows whose width, strides or base addresses are not multiples of
-// 16 bytes take the same code with single-element accesses (VEC = 1, the wavefront's 64 lanes side by side).
+// by lane shuffles, across wavefronts through LDS.  Rows of any width, stride and alignment take the same 16-byte
+// accesses, at the element's alignment; only a row's last few elements go one by one.
 // Statistics: the mean first, then the squares of the differences, both in fp32 from registers: no cancellation of
 // E[s^2] - m^2.
 //
@@ -51,72 +51,95 @@ struct BwdArgs {
   const float *mean, *rstd;
   uint8_t* dx;
   float* part;  // [2][G][H]: weight partials, then bias partials
-  bool want_bias;
 };
 
-// VEC consecutive elements as fp32: bf16 (ESZ 2) or fp32 (ESZ 4)
-template <int ESZ, int VEC>
-MOE_DEV void load_vec(const uint8_t* p, float (&v)[VEC]) {
-  if constexpr (VEC == 1) {
-    v[0] = ESZ == 4 ? *reinterpret_cast<const float*>(p)
-                    : __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t*>(p) << 16);
-  } else {
-    constexpr int ND = VEC * ESZ / 4;  // dwords: 2, 4 or 8
-    int q[ND];
-    if constexpr (ND == 2) {
-      const i32x2_t d = *reinterpret_cast<const i32x2_t*>(p);
-      q[0] = d[0];
-      q[1] = d[1];
-    } else {
-#pragma unroll
-      for (int k = 0; k < ND / 4; ++k) {
-        const i32x4_t d = reinterpret_cast<const i32x4_t*>(p)[k];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) q[4 * k + x] = d[x];
-      }
-    }
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      if constexpr (ESZ == 4) {
-        v[e] = __int_as_float(q[e]);
-      } else {
-        const uint32_t u = (uint32_t)q[e / 2];
-        v[e] = __uint_as_float(e & 1 ? u & 0xFFFF0000u : u << 16);
-      }
-    }
-  }
-}
-template <int ESZ, int VEC>
-MOE_DEV void store_vec(uint8_t* p, const float (&v)[VEC]) {
-  if constexpr (VEC == 1) {
+// 16 bytes of a row (VEC = 16 / ESZ elements), at the elements' own alignment: one wide access, which the memory system
+// splits where it crosses a line.  TAIL: H is no multiple of VEC, and a row's last elements go one by one (a variant of its
+// own: the code for them costs every width 20 to 50 registers, and with them resident wavefronts).
+typedef int i32x4_e4_t __attribute__((ext_vector_type(4), aligned(4)));
+typedef int i32x4_e2_t __attribute__((ext_vector_type(4), aligned(2)));
+
+template <int ESZ, bool TAIL>
+MOE_DEV i32x4_t load_row16(const uint8_t* row, int c, int H) {
+  constexpr int VEC = 16 / ESZ;
+  const uint8_t* p = row + (uint32_t)(c * ESZ);
+  i32x4_t q = {0, 0, 0, 0};
+  if (c + VEC <= H) {
     if constexpr (ESZ == 4)
-      *reinterpret_cast<float*>(p) = v[0];
+      q = *reinterpret_cast<const i32x4_e4_t*>(p);
     else
-      *reinterpret_cast<uint16_t*>(p) = f32_to_bf16_bits(v[0]);
-  } else {
-    constexpr int NW = VEC * ESZ / 16;
+      q = *reinterpret_cast<const i32x4_e2_t*>(p);
+  } else if (TAIL && c < H) {
 #pragma unroll
-    for (int k = 0; k < NW; ++k) {
-      i32x4_t q;
-#pragma unroll
-      for (int d = 0; d < 4; ++d) {
+    for (int e = 0; e < VEC - 1; ++e)
+      if (c + e < H) {
         if constexpr (ESZ == 4)
-          q[d] = __float_as_int(v[k * 4 + d]);
+          q[e] = reinterpret_cast<const int*>(p)[e];
         else
-          q[d] = (int)((uint32_t)f32_to_bf16_bits(v[k * 8 + 2 * d]) |
-                       ((uint32_t)f32_to_bf16_bits(v[k * 8 + 2 * d + 1]) << 16));
+          q[e / 2] |= (int)((uint32_t)reinterpret_cast<const uint16_t*>(p)[e] << (16 * (e & 1)));
       }
-      reinterpret_cast<i32x4_t*>(p)[k] = q;
+  }
+  return q;
+}
+template <int ESZ>
+MOE_DEV float element(const i32x4_t& q, int e) {
+  if constexpr (ESZ == 4) return __int_as_float(q[e]);
+  const uint32_t u = (uint32_t)q[e / 2];
+  return __uint_as_float(e & 1 ? u & 0xFFFF0000u : u << 16);
+}
+template <int ESZ, bool TAIL, int VEC>
+MOE_DEV void store_row16(uint8_t* row, int c, int H, const float (&v)[VEC]) {
+  uint8_t* p = row + (uint32_t)(c * ESZ);
+  if (c + VEC <= H) {
+    i32x4_t q;
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+      if constexpr (ESZ == 4)
+        q[d] = __float_as_int(v[d]);
+      else
+        q[d] = (int)((uint32_t)f32_to_bf16_bits(v[2 * d]) | ((uint32_t)f32_to_bf16_bits(v[2 * d + 1]) << 16));
+    }
+    if constexpr (ESZ == 4)
+      *reinterpret_cast<i32x4_e4_t*>(p) = q;
+    else
+      *reinterpret_cast<i32x4_e2_t*>(p) = q;
+  } else if (TAIL && c < H) {
+#pragma unroll
+    for (int e = 0; e < VEC - 1; ++e)
+      if (c + e < H) {
+        if constexpr (ESZ == 4)
+          reinterpret_cast<float*>(p)[e] = v[e];
+        else
+          reinterpret_cast<uint16_t*>(p)[e] = f32_to_bf16_bits(v[e]);
+      }
+  }
+}
+// VEC columns of the weight or bias: fp32 or bf16 by a launch-uniform flag; 0 past H
+template <int VEC, bool TAIL>
+MOE_DEV void load_param(const uint8_t* p, bool bf16, int c, int H, float (&v)[VEC]) {
+  if (bf16 && VEC == 8) {
+    const i32x4_t q = load_row16<2, TAIL>(p, c, H);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) v[e] = element<2>(q, e);
+  } else if (bf16) {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e)
+      v[e] = c + e < H ? __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(p)[c + e] << 16) : 0.0f;
+  } else {
+#pragma unroll
+    for (int d = 0; d < VEC / 4; ++d) {
+      const i32x4_t q = load_row16<4, TAIL>(p, c + 4 * d, H);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[4 * d + e] = element<4>(q, e);
     }
   }
 }
-// weight or bias columns: fp32 or bf16 by a launch-uniform flag
-template <int VEC>
-MOE_DEV void load_param(const uint8_t* p, bool bf16, int c, float (&v)[VEC]) {
-  if (bf16)
-    load_vec<2, VEC>(p + (int64_t)c * 2, v);
-  else
-    load_vec<4, VEC>(p + (int64_t)c * 4, v);
+
+// The row group of this thread; one per wavefront or several wavefronts per group: a scalar, and the row's addresses with it.
+template <int TPR>
+MOE_DEV int row_group() {
+  if constexpr (TPR >= 64) return uniform_int(threadIdx.x / TPR);
+  return threadIdx.x / TPR;
 }
 
 // Sum of one or two values over the TPR threads of a row, to all of them, in a fixed order.  `red` has a slot per
@@ -147,43 +170,38 @@ MOE_DEV void row_sum(float (&v)[N], float (*red)[THREADS / 64 * 2], int& flip) {
   }
 }
 
-template <int ESZ, int VEC, int NV, int TPR>
+template <int ESZ, int NV, int TPR, bool TAIL>
 __global__ __launch_bounds__((TPR < 256 ? 256 : TPR)) void norm_fwd_kernel(const FwdArgs a) {
   constexpr int THREADS = TPR < 256 ? 256 : TPR;
-  constexpr int RPB = THREADS / TPR;
+  constexpr int RPB = THREADS / TPR, VEC = 16 / ESZ;
   __shared__ float red[2][THREADS / 64 * 2];
   int flip = 0;
   const int t = threadIdx.x % TPR;
-  const int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
+  const int64_t row = (int64_t)blockIdx.x * RPB + row_group<TPR>();
   const bool live = row < a.T;
   const int64_t rr = live ? row : a.T - 1;  // surplus threads compute the last row and store nothing
+  i32x4_t raw[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) raw[i] = load_row16<ESZ, TAIL>(a.x + rr * a.ldx * ESZ, (i * TPR + t) * VEC, a.H);
   float v[NV][VEC];
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (i * TPR + t) * VEC;
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) v[i][e] = 0.0f;
-    if (c < a.H) load_vec<ESZ, VEC>(a.x + (rr * a.ldx + c) * ESZ, v[i]);
-  }
   if (a.res != nullptr) {
-    float u[NV][VEC];
+    i32x4_t res[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) res[i] = load_row16<ESZ, TAIL>(a.res + rr * a.ldr * ESZ, (i * TPR + t) * VEC, a.H);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = (i * TPR + t) * VEC;
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) u[i][e] = 0.0f;
-      if (c < a.H) load_vec<ESZ, VEC>(a.res + (rr * a.ldr + c) * ESZ, u[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (i * TPR + t) * VEC;
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
-        v[i][e] += u[i][e];
+        v[i][e] = element<ESZ>(raw[i], e) + element<ESZ>(res[i], e);
         if constexpr (ESZ == 2) v[i][e] = __uint_as_float((uint32_t)f32_to_bf16_bits(v[i][e]) << 16);
       }
-      if (c < a.H && live) store_vec<ESZ, VEC>(a.sum + (row * a.H + c) * ESZ, v[i]);
+      if (live) store_row16<ESZ, TAIL, VEC>(a.sum + row * a.H * ESZ, (i * TPR + t) * VEC, a.H, v[i]);
     }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) v[i][e] = element<ESZ>(raw[i], e);
   }
   const float h = (float)a.H;
   float m = 0.0f;
@@ -198,14 +216,12 @@ __global__ __launch_bounds__((TPR < 256 ? 256 : TPR)) void norm_fwd_kernel(const
   }
   float s2[1] = {0.0f};
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const bool in = (i * TPR + t) * VEC < a.H;
+  for (int i = 0; i < NV; ++i)
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
-      const float d = in ? v[i][e] - m : 0.0f;
-      s2[0] = __builtin_fmaf(d, d, s2[0]);
+      v[i][e] = (i * TPR + t) * VEC + (TAIL ? e : 0) < a.H ? v[i][e] - m : 0.0f;
+      s2[0] = __builtin_fmaf(v[i][e], v[i][e], s2[0]);
     }
-  }
   row_sum<TPR, THREADS, 1>(s2, red, flip);
   const float r = 1.0f / sqrtf(s2[0] / h + a.eps);
   if (t == 0 && live) {
@@ -215,172 +231,189 @@ __global__ __launch_bounds__((TPR < 256 ? 256 : TPR)) void norm_fwd_kernel(const
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int c = (i * TPR + t) * VEC;
-    const bool in = c < a.H;
     float w[VEC], y[VEC];
-    if (in) {
-      load_param<VEC>(a.w, a.w_bf16, c, w);
+    load_param<VEC, TAIL>(a.w, a.w_bf16, c, a.H, w);
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) y[e] = (v[i][e] - m) * r * w[e];
-      if (a.b != nullptr) {
-        load_param<VEC>(a.b, a.w_bf16, c, w);
+    for (int e = 0; e < VEC; ++e) y[e] = v[i][e] * r * w[e];
+    if (a.b != nullptr) {
+      load_param<VEC, TAIL>(a.b, a.w_bf16, c, a.H, w);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) y[e] += w[e];
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) y[e] = 0.0f;
+      for (int e = 0; e < VEC; ++e) y[e] += w[e];
     }
-    if constexpr (VEC > 1) {
-      if (a.y_fp8) {
-        // one scale per 128 columns: 128 / VEC consecutive lanes (16 for bf16 rows, 32 for fp32 rows)
-        float amax = 0.0f;
+    if (a.y_fp8) {
+      // one scale per 128 columns: 128 / VEC consecutive lanes (16 for bf16 rows, 32 for fp32 rows); H % 128 == 0
+      float amax = 0.0f;
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) amax = fmaxf(amax, fabsf(y[e]));
+      for (int e = 0; e < VEC; ++e) amax = fmaxf(amax, c < a.H ? fabsf(y[e]) : 0.0f);
 #pragma unroll
-        for (int o = 64 / VEC; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor(amax, o, 64));
-        const float sc = amax > 0.0f ? amax / 448.0f : 1.0f;
-        if (in && live) {
-          uint32_t code[VEC / 4];
+      for (int o = 64 / VEC; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor(amax, o, 64));
+      const float sc = amax > 0.0f ? amax / 448.0f : 1.0f;
+      if (c < a.H && live) {
+        uint32_t code[VEC / 4];
 #pragma unroll
-          for (int q = 0; q < VEC / 4; ++q) {
-            float d[4];
+        for (int q = 0; q < VEC / 4; ++q) {
+          float d[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) d[e] = y[q * 4 + e] / sc;
-            code[q] = f32x2_to_e4m3x2(d[0], d[1]) | (f32x2_to_e4m3x2(d[2], d[3]) << 16);
+          for (int e = 0; e < 4; ++e) d[e] = y[q * 4 + e] / sc;
+          code[q] = f32x2_to_e4m3x2(d[0], d[1]) | (f32x2_to_e4m3x2(d[2], d[3]) << 16);
 #pragma unroll
-            for (int e = 0; e < 4; ++e)  // the clamp of the conversion takes NaN for a number: its code is set here
-              if (d[e] != d[e]) code[q] = (code[q] & ~(0xFFu << (8 * e))) | (0x7Fu << (8 * e));
-          }
-          uint32_t* dst = reinterpret_cast<uint32_t*>(a.y + row * a.H + c);
-#pragma unroll
-          for (int q = 0; q < VEC / 4; ++q) dst[q] = code[q];
-          if (c % 128 == 0) a.ys[row * (a.H / 128) + c / 128] = sc;
+          for (int e = 0; e < 4; ++e)  // the clamp of the conversion takes NaN for a number: its code is set here
+            if (d[e] != d[e]) code[q] = (code[q] & ~(0xFFu << (8 * e))) | (0x7Fu << (8 * e));
         }
-        continue;
+        uint32_t* dst = reinterpret_cast<uint32_t*>(a.y + row * a.H + c);
+        if constexpr (VEC == 8)
+          *reinterpret_cast<i32x2_t*>(dst) = (i32x2_t){(int)code[0], (int)code[1]};
+        else
+          dst[0] = code[0];
+        if (c % 128 == 0) a.ys[row * (a.H / 128) + c / 128] = sc;
       }
+    } else if (live) {
+      store_row16<ESZ, TAIL, VEC>(a.y + row * a.H * ESZ, c, a.H, y);
     }
-    if (in && live) store_vec<ESZ, VEC>(a.y + (row * a.H + c) * ESZ, y);
   }
 }
 
-template <int ESZ, int VEC, int NV, int TPR>
+// BIAS: whether the bias's gradient is wanted (its sums take as many registers as the weight's)
+template <int ESZ, int NV, int TPR, bool TAIL, bool BIAS>
 __global__ __launch_bounds__((TPR < 256 ? 256 : TPR)) void norm_bwd_kernel(const BwdArgs a) {
   constexpr int THREADS = TPR < 256 ? 256 : TPR;
-  constexpr int RPB = THREADS / TPR;
+  constexpr int RPB = THREADS / TPR, VEC = 16 / ESZ, WAVES = THREADS / 64;
+  constexpr int COLS = TPR * NV * VEC;
+  // wavefronts that hold the same columns: their sums meet in LDS
+  constexpr int SHARE = TPR < 64 ? WAVES : RPB, PER = WAVES / SHARE;
   __shared__ float red[2][THREADS / 64 * 2];
-  __shared__ float comb[RPB > 1 ? TPR * NV * VEC : 1];  // sums of one column range, the groups added one by one
+  __shared__ float comb[SHARE > 1 ? SHARE * COLS : 1];
   int flip = 0;
-  const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
-  const float inv_h = 1.0f / (float)a.H;
-  float dw[NV][VEC], db[NV][VEC], w[NV][VEC];
+  const int t = threadIdx.x % TPR, sub = row_group<TPR>();
+  const float h = (float)a.H;
+  float dw[NV][VEC], db[BIAS ? NV : 1][VEC], w[NV][VEC];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int c = (i * TPR + t) * VEC;
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) dw[i][e] = db[i][e] = w[i][e] = 0.0f;
-    if (c < a.H) load_param<VEC>(a.w, a.w_bf16, c, w[i]);
+    for (int e = 0; e < VEC; ++e) {
+      dw[i][e] = 0.0f;
+      if constexpr (BIAS) db[i][e] = 0.0f;
+    }
+    load_param<VEC, TAIL>(a.w, a.w_bf16, (i * TPR + t) * VEC, a.H, w[i]);
   }
-  for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < a.T; r0 += (int64_t)gridDim.x * RPB) {
+  const int64_t step = (int64_t)gridDim.x * RPB;
+  i32x4_t qy[NV], qs[NV];  // the next row, loaded while the one before is summed
+  float m = 0.0f, r = 0.0f;
+  auto fetch = [&](int64_t r0) {
+    const int64_t row = r0 + sub < a.T ? r0 + sub : a.T - 1;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * TPR + t) * VEC;
+      qy[i] = load_row16<ESZ, TAIL>(a.dy + row * a.ld_dy * ESZ, c, a.H);
+      qs[i] = load_row16<ESZ, TAIL>(a.s + row * a.ld_s * ESZ, c, a.H);
+    }
+    if (!a.rms) m = a.mean[row];
+    r = a.rstd[row];
+  };
+  int64_t r0 = (int64_t)blockIdx.x * RPB;
+  if (r0 < a.T) fetch(r0);
+  for (; r0 < a.T; r0 += step) {
     const int64_t row = r0 + sub;
     const bool live = row < a.T;
-    const int64_t rr = live ? row : a.T - 1;
-    float z[NV][VEC], dy[NV][VEC];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (i * TPR + t) * VEC;
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) z[i][e] = dy[i][e] = 0.0f;
-      if (c < a.H && live) {
-        load_vec<ESZ, VEC>(a.dy + (rr * a.ld_dy + c) * ESZ, dy[i]);
-        load_vec<ESZ, VEC>(a.s + (rr * a.ld_s + c) * ESZ, z[i]);
-      }
-    }
-    const float m = a.rms ? 0.0f : a.mean[rr];
-    const float r = a.rstd[rr];
+    float z[NV][VEC], tw[NV][VEC];
+    const float rs = r;
     float c12[2] = {0.0f, 0.0f};
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const bool in = (i * TPR + t) * VEC < a.H && live;
+    for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
-        z[i][e] = in ? (z[i][e] - m) * r : 0.0f;
-        dw[i][e] = __builtin_fmaf(dy[i][e], z[i][e], dw[i][e]);
-        db[i][e] += dy[i][e];
-        const float tw = dy[i][e] * w[i][e];
-        c12[0] += tw;
-        c12[1] = __builtin_fmaf(tw, z[i][e], c12[1]);
+        const bool in = (i * TPR + t) * VEC + (TAIL ? e : 0) < a.H && live;
+        const float dy = in ? element<ESZ>(qy[i], e) : 0.0f;
+        z[i][e] = in ? (element<ESZ>(qs[i], e) - m) * rs : 0.0f;
+        dw[i][e] = __builtin_fmaf(dy, z[i][e], dw[i][e]);
+        if constexpr (BIAS) db[i][e] += dy;
+        tw[i][e] = dy * w[i][e];
+        c12[0] += tw[i][e];
+        c12[1] = __builtin_fmaf(tw[i][e], z[i][e], c12[1]);
       }
-    }
-    row_sum<TPR, THREADS, 2>(c12, red, flip);
-    const float c1 = a.rms ? 0.0f : c12[0] * inv_h, c2 = c12[1] * inv_h;
+    i32x4_t qd[NV];
+    if (a.dsum != nullptr) {
+      const int64_t rr = live ? row : a.T - 1;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (i * TPR + t) * VEC;
-      if (c < a.H && live) {
+      for (int i = 0; i < NV; ++i) qd[i] = load_row16<ESZ, TAIL>(a.dsum + rr * a.ld_dsum * ESZ, (i * TPR + t) * VEC, a.H);
+    }
+    if (r0 + step < a.T) fetch(r0 + step);
+    row_sum<TPR, THREADS, 2>(c12, red, flip);
+    const float c1 = a.rms ? 0.0f : c12[0] / h, c2 = c12[1] / h;
+    if (live)
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
         float d[VEC];
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) d[e] = (dy[i][e] * w[i][e] - c1 - z[i][e] * c2) * r;
-        if (a.dsum != nullptr) {
-          float u[VEC];
-          load_vec<ESZ, VEC>(a.dsum + (row * a.ld_dsum + c) * ESZ, u);
+        for (int e = 0; e < VEC; ++e) d[e] = (tw[i][e] - c1 - z[i][e] * c2) * rs;
+        if (a.dsum != nullptr)
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) d[e] += u[e];
-        }
-        store_vec<ESZ, VEC>(a.dx + (row * a.H + c) * ESZ, d);
+          for (int e = 0; e < VEC; ++e) d[e] += element<ESZ>(qd[i], e);
+        store_row16<ESZ, TAIL, VEC>(a.dx + row * a.H * ESZ, (i * TPR + t) * VEC, a.H, d);
       }
-    }
   }
-  // one partial row per workgroup
+  // one partial row per workgroup: the row groups of a wavefront are added by lane exchanges, the wavefronts in LDS
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    if (k == 1 && !a.want_bias) break;
+  for (int k = 0; k < (BIAS ? 2 : 1); ++k) {
     float* out = a.part + ((int64_t)k * gridDim.x + blockIdx.x) * a.H;
-    if constexpr (RPB > 1) {
-      for (int g = RPB - 1; g >= 0; --g) {
-        __syncthreads();
-        if (sub == g) {
+    float v[NV][VEC];
 #pragma unroll
-          for (int i = 0; i < NV; ++i)
+    for (int i = 0; i < NV; ++i)
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-              const int c = (i * TPR + t) * VEC + e;
-              const float v = (k == 0 ? dw[i][e] : db[i][e]) + (g == RPB - 1 ? 0.0f : comb[c]);
-              if (g > 0)
-                comb[c] = v;
-              else if (c < a.H)
-                out[c] = v;
-            }
-        }
+      for (int e = 0; e < VEC; ++e) {
+        v[i][e] = k == 0 ? dw[i][e] : db[BIAS ? i : 0][e];
+#pragma unroll
+        for (int o = TPR; o < 64; o <<= 1) v[i][e] += __shfl_xor(v[i][e], o, 64);
+      }
+    if constexpr (SHARE > 1) {
+      if (k > 0) __syncthreads();
+      const int share = (threadIdx.x >> 6) / PER;
+      if (TPR >= 64 || (threadIdx.x & 63) < TPR)
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) comb[share * COLS + (i * TPR + t) * VEC + e] = v[i][e];
+      __syncthreads();
+      for (int c = threadIdx.x; c < COLS; c += THREADS) {
+        float s = 0.0f;
+#pragma unroll
+        for (int q = 0; q < SHARE; ++q) s += comb[q * COLS + c];
+        if (c < a.H) out[c] = s;
       }
     } else {
 #pragma unroll
       for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          const int c = (i * TPR + t) * VEC + e;
-          if (c < a.H) out[c] = k == 0 ? dw[i][e] : db[i][e];
-        }
+        for (int d = 0; d < VEC / 4; ++d)
+          store_row16<4, TAIL, 4>(reinterpret_cast<uint8_t*>(out), (i * TPR + t) * VEC + 4 * d, a.H,
+                            reinterpret_cast<const float(&)[4]>(v[i][4 * d]));
     }
   }
 }
 
-// out[c] = sum over the G partial rows, in a fixed order: 32 columns and 32 row lanes per workgroup.  blockIdx.y: 0 the
-// weight's partials, 1 the bias's.  G = 0 (no rows) writes zeros.
-__global__ __launch_bounds__(1024) void norm_reduce_kernel(const float* __restrict__ part, int G, int H,
-                                                           float* __restrict__ dw, float* __restrict__ db) {
+// out[c] = sum over the G partial rows, in a fixed order: 32 columns (8 threads of 4) and 32 row lanes per workgroup.
+// blockIdx.y: 0 the weight's partials, 1 the bias's.  G = 0 (no rows) writes zeros.
+__global__ __launch_bounds__(256) void norm_reduce_kernel(const float* __restrict__ part, int G, int H,
+                                                          float* __restrict__ dw, float* __restrict__ db) {
   __shared__ float red[32][33];
-  const int c = blockIdx.x * 32 + (threadIdx.x & 31), g0 = threadIdx.x >> 5;
-  const float* p = part + (int64_t)blockIdx.y * G * H;
-  float s = 0.0f;
-  if (c < H)
-    for (int g = g0; g < G; g += 32) s += p[(int64_t)g * H + c];
-  red[g0][threadIdx.x & 31] = s;
+  const int q = threadIdx.x & 7, g0 = threadIdx.x >> 3, c = blockIdx.x * 32 + q * 4;
+  const uint8_t* p = reinterpret_cast<const uint8_t*>(part + (int64_t)blockIdx.y * G * H);
+  float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+  for (int g = g0; g < G; g += 32) {
+    const i32x4_t v = load_row16<4, true>(p + (int64_t)g * H * 4, c, H);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s[e] += __int_as_float(v[e]);
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) red[g0][q * 4 + e] = s[e];
   __syncthreads();
-  if (threadIdx.x < 32 && c < H) {
+  const int col = blockIdx.x * 32 + (int)threadIdx.x;
+  if (threadIdx.x < 32 && col < H) {
     float v = 0.0f;
 #pragma unroll
     for (int g = 0; g < 32; ++g) v += red[g][threadIdx.x];
-    (blockIdx.y == 0 ? dw : db)[c] = v;
+    (blockIdx.y == 0 ? dw : db)[col] = v;
   }
 }
 
@@ -395,55 +428,54 @@ static int rows_per_block(int H) {
   return t < 256 ? 256 / t : 1;
 }
 
-template <int ESZ, int VEC, bool BWD, typename Args>
-static void launch_shape(const Args& a, int tpr, unsigned grid, hipStream_t s) {
-#define MOE_NORM_LAUNCH(NV, TPR)                                                                        \
-  do {                                                                                                  \
-    constexpr int TH = TPR < 256 ? 256 : TPR;                                                           \
-    if constexpr (BWD)                                                                                  \
-      hipLaunchKernelGGL((norm_bwd_kernel<ESZ, VEC, NV, TPR>), dim3(grid), dim3(TH), 0, s, a);          \
-    else                                                                                                \
-      hipLaunchKernelGGL((norm_fwd_kernel<ESZ, VEC, NV, TPR>), dim3(grid), dim3(TH), 0, s, a);          \
-  } while (0)
-  if (a.H > 16384) {
-    MOE_NORM_LAUNCH(64 / VEC, 1024);
-    return;
-  }
-  switch (tpr) {
-    case 16: MOE_NORM_LAUNCH(16 / VEC, 16); break;
-    case 32: MOE_NORM_LAUNCH(16 / VEC, 32); break;
-    case 64: MOE_NORM_LAUNCH(16 / VEC, 64); break;
-    case 128: MOE_NORM_LAUNCH(16 / VEC, 128); break;
-    case 256: MOE_NORM_LAUNCH(16 / VEC, 256); break;
-    case 512: MOE_NORM_LAUNCH(16 / VEC, 512); break;
-    default: MOE_NORM_LAUNCH(16 / VEC, 1024); break;
-  }
-#undef MOE_NORM_LAUNCH
+enum Kind { FWD, BWD, BWD_BIAS };
+
+template <int ESZ, Kind KIND, bool TAIL, int NV, int TPR, typename Args>
+static void launch_tail(const Args& a, unsigned grid, hipStream_t s) {
+  constexpr int TH = TPR < 256 ? 256 : TPR;
+  if constexpr (KIND == FWD)
+    hipLaunchKernelGGL((norm_fwd_kernel<ESZ, NV, TPR, TAIL>), dim3(grid), dim3(TH), 0, s, a);
+  else
+    hipLaunchKernelGGL((norm_bwd_kernel<ESZ, NV, TPR, TAIL, KIND == BWD_BIAS>), dim3(grid), dim3(TH), 0, s, a);
 }
 
-static bool vec_ok(const void* p, int64_t ld, int esz) {
-  return p == nullptr || (((uintptr_t)p % 16) == 0 && (ld * esz) % 16 == 0);
+template <int ESZ, Kind KIND, int NV, int TPR, typename Args>
+static void launch_tpr(const Args& a, unsigned grid, hipStream_t s) {
+  if (a.H % (16 / ESZ) != 0)
+    launch_tail<ESZ, KIND, true, NV, TPR>(a, grid, s);
+  else
+    launch_tail<ESZ, KIND, false, NV, TPR>(a, grid, s);
+}
+
+template <int ESZ, Kind KIND, typename Args>
+static void launch_shape(const Args& a, int tpr, unsigned grid, hipStream_t s) {
+  constexpr int NV = ESZ;  // 16 columns per thread
+  if (a.H > 16384) return launch_tpr<ESZ, KIND, 4 * NV, 1024>(a, grid, s);
+  switch (tpr) {
+    case 16: return launch_tpr<ESZ, KIND, NV, 16>(a, grid, s);
+    case 32: return launch_tpr<ESZ, KIND, NV, 32>(a, grid, s);
+    case 64: return launch_tpr<ESZ, KIND, NV, 64>(a, grid, s);
+    case 128: return launch_tpr<ESZ, KIND, NV, 128>(a, grid, s);
+    case 256: return launch_tpr<ESZ, KIND, NV, 256>(a, grid, s);
+    case 512: return launch_tpr<ESZ, KIND, NV, 512>(a, grid, s);
+    default: return launch_tpr<ESZ, KIND, NV, 1024>(a, grid, s);
+  }
 }
 
 }  // namespace norm
 
-// Workgroups of the backward pass: at most four of 256 threads' worth per compute unit (256 of them), so the partial
-// rows stay a few percent of the traffic.
+// Workgroups of the backward pass.  Two of 256 threads or one larger one per compute unit: with the next row on its way
+// while a row is summed that many keep the memory busy, and the partial rows stay a few percent of the traffic
+// (16384 x 4096 bf16 with bias: 512 workgroups 81 us, 1024 95 us, 256 128 us).  And no more than leaves each four passes
+// over its rows (2048 x 4096: 512 workgroups 18.5 us, 1024 19.8 us), but at least one per compute unit.
 int norm_backward_groups(int64_t T, int H) {
   const int rpb = norm::rows_per_block(H);
   const int tpr = norm::threads_per_row(H);
-  const int64_t most = tpr <= 256 ? 1024 : tpr == 512 ? 512 : 256;
+  const int64_t most = tpr <= 256 ? 512 : 256;
   const int64_t need = (T + rpb - 1) / rpb;
-  return (int)(need < most ? need : most);
-}
-
-bool norm_vector_ok(const NormLaunch& p) {
-  const int esz = p.dtype == MOE_DTYPE_F32 ? 4 : 2, wsz = p.w_bf16 ? 2 : 4;
-  const int vec = 16 / esz;
-  return p.H % vec == 0 && (p.H * wsz) % 16 == 0 && norm::vec_ok(p.x, p.ldx, esz) &&
-         norm::vec_ok(p.residual, p.ldr, esz) && norm::vec_ok(p.dy, p.ld_dy, esz) &&
-         norm::vec_ok(p.weight, 0, wsz) && norm::vec_ok(p.bias, 0, wsz) && norm::vec_ok(p.sum, p.H, esz) &&
-         norm::vec_ok(p.y, 0, 1) && norm::vec_ok(p.dx, 0, 1);
+  int64_t g = need / 4;
+  if (g < 256) g = need < 256 ? need : 256;
+  return (int)(g < most ? g : most);
 }
 
 void launch_norm(const NormLaunch& p, hipStream_t s) {
@@ -470,11 +502,10 @@ void launch_norm(const NormLaunch& p, hipStream_t s) {
   if (p.y_fp8 && f32 && tpr < 32) tpr = 32;  // a 128-column block of fp32 rows spans 32 lanes
   const int rpb = tpr < 256 ? 256 / tpr : 1;
   const unsigned grid = (unsigned)((p.T + rpb - 1) / rpb);
-  const bool vec = norm_vector_ok(p);
   if (f32)
-    vec ? norm::launch_shape<4, 4, false>(a, tpr, grid, s) : norm::launch_shape<4, 1, false>(a, tpr, grid, s);
+    norm::launch_shape<4, norm::FWD>(a, tpr, grid, s);
   else
-    vec ? norm::launch_shape<2, 8, false>(a, tpr, grid, s) : norm::launch_shape<2, 1, false>(a, tpr, grid, s);
+    norm::launch_shape<2, norm::FWD>(a, tpr, grid, s);
 }
 
 void launch_norm_backward(const NormLaunch& p, hipStream_t s) {
@@ -494,18 +525,17 @@ void launch_norm_backward(const NormLaunch& p, hipStream_t s) {
   a.rstd = p.rstd;
   a.dx = (uint8_t*)p.dx;
   a.part = p.part;
-  a.want_bias = p.dbias != nullptr;
   const int tpr = norm::threads_per_row(p.H);
   const int G = norm_backward_groups(p.T, p.H);
   if (G > 0) {
-    const bool vec = norm_vector_ok(p);
-    if (p.dtype == MOE_DTYPE_F32)
-      vec ? norm::launch_shape<4, 4, true>(a, tpr, G, s) : norm::launch_shape<4, 1, true>(a, tpr, G, s);
+    const bool f32 = p.dtype == MOE_DTYPE_F32, bias = p.dbias != nullptr;
+    if (f32)
+      bias ? norm::launch_shape<4, norm::BWD_BIAS>(a, tpr, G, s) : norm::launch_shape<4, norm::BWD>(a, tpr, G, s);
     else
-      vec ? norm::launch_shape<2, 8, true>(a, tpr, G, s) : norm::launch_shape<2, 1, true>(a, tpr, G, s);
+      bias ? norm::launch_shape<2, norm::BWD_BIAS>(a, tpr, G, s) : norm::launch_shape<2, norm::BWD>(a, tpr, G, s);
   }
   hipLaunchKernelGGL(norm::norm_reduce_kernel, dim3((unsigned)((p.H + 31) / 32), p.dbias != nullptr ? 2 : 1),
-                     dim3(1024), 0, s, p.part, G, p.H, p.dweight, p.dbias);
+                     dim3(256), 0, s, p.part, G, p.H, p.dweight, p.dbias);
 }
 
 }  // namespace moe

@@ -377,9 +377,9 @@ moe_status moe_grouped_ffn_backward(const void* dout, int64_t T, int32_t k, int3
  *   y        (device) [T, H] contiguous out, y_dtype: dtype, or FP8_E4M3 with y_scales (device) [T, H/128] fp32 out,
  *            the form moe_dispatch_permute takes: per row and 128 columns scale = amax / 448 (amax over the values
  *            that are not NaN; 1 where amax is 0), code = y / scale rounded to nearest even, NaN kept.  FP8_E4M3
- *            needs H % 128 == 0 and 16-byte aligned rows and parameters.  y_scales is unused otherwise.
+ *            needs H % 128 == 0 and a 16-byte aligned y.  y_scales is unused otherwise.
  *   mean, rstd (device) [T] fp32 out, each may be NULL; mean is not written for MOE_NORM_RMS.
- * Alignment: the element size (16-byte aligned rows and parameters take wide accesses).
+ * Alignment: the element size.
  * Domain: 0 <= T < 2^31, 1 <= H <= 65536, eps >= 0 and finite.
  */
 typedef enum { MOE_NORM_LAYER = 0, MOE_NORM_RMS = 1 } moe_norm_kind;

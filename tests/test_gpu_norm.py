@@ -137,10 +137,7 @@ def test_strides_offsets_and_canaries(dt):
         check_forward(r, x, w, b, res, "layer", 1e-5)
         assert (buf[:32] == -7).all() and (buf[32 + T * H:] == -7).all()
         c = m.moe_norm(x.contiguous(), w, b, res.contiguous(), "layer", 1e-5)
-        # a row's sums are added in another order where an operand cannot take wide accesses: bit for bit only with them
-        # (bfloat16 rows at 540 values are 8-byte aligned, float32 rows 16-byte)
-        if all(t.data_ptr() % 16 == 0 for t in (x, res)):
-            assert torch.equal(c.y, r.y) and torch.equal(c.rstd, r.rstd)
+        assert torch.equal(c.y, r.y) and torch.equal(c.rstd, r.rstd)
         ref[off] = r
         dbuf = torch.full((T * H + 64,), -7.0, device="cuda", dtype=dt)
         out = dict(dx=dbuf[32:32 + T * H].view(T, H), dweight=torch.empty(H, device="cuda"),
@@ -148,6 +145,15 @@ def test_strides_offsets_and_canaries(dt):
         m.moe_norm_backward(res, r.sum, w, r.mean, r.rstd, dsum=x, out=out)
         assert (dbuf[:32] == -7).all() and (dbuf[32 + T * H:] == -7).all()
         check_backward(out, res, r.sum, w, r.mean, r.rstd, "layer", x)
+
+
+def test_unaligned_rows_to_e4m3():
+    T, H = 21, 384
+    wide = normal(4, T, 2 * H + 30).bfloat16()
+    w = normal(6, H + 1).bfloat16()[1:]
+    x, res = wide[:, 1:1 + H], wide[:, H + 7:2 * H + 7]
+    r = m.moe_norm(x, w, residual=res, kind="rms", out_dtype=torch.uint8)
+    check_forward(r, x, w, None, res, "rms", 1e-5)
 
 
 @pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
