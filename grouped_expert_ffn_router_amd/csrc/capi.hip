@@ -752,15 +752,15 @@ size_t moe_orthogonalize_workspace_bytes(int64_t batch, int32_t m, int32_t n, mo
 }
 
 // Whether `steps` of s -> s (a + b s^2 + c s^4) from [0, 1] stay where the fp16 operands hold them: |s| <= 3, and
-// |b s^2 + c s^4| <= 12 (the operands carry a factor 2^12, and fp16 ends at 16 * 2^12).  The bounds are taken at 4097
+// |a + b s^2 + c s^4| <= 12 (the operands carry a factor 2^12, and fp16 ends at 16 * 2^12).  The bounds are taken at 4097
 // points of each step's interval, with a factor 1.01 between steps for what lies between the points.
 static bool iteration_bounded(int32_t steps, float a, float b, float c) {
   double hi = 1.0;
   for (int32_t k = 0; k < steps; ++k) {
     double next = 0.0;
     for (int i = 0; i <= 4096; ++i) {
-      const double s = hi * i / 4096, s2 = s * s, q = (double)b * s2 + (double)c * s2 * s2;
-      const double v = s * ((double)a + q);
+      const double s = hi * i / 4096, s2 = s * s, q = (double)a + (double)b * s2 + (double)c * s2 * s2;
+      const double v = s * q;
       if (!(q <= 12.0 && q >= -12.0 && v <= 3.0 && v >= -3.0)) return false;
       next = v > next ? v : (-v > next ? -v : next);
     }

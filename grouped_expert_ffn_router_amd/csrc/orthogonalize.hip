@@ -68,24 +68,25 @@ struct Cfg<2, true> {
 constexpr int TILE[3] = {64, 128, 256};
 
 struct Args {
-  // operands: hi and (SPLIT) lo, [rows][K] fp16 per matrix of the batch
+  // operands: hi and (SPLIT) lo, fp16.  GRAM: [K][rows] per matrix of the batch (the reduction runs over rows); else [rows][K]
   const uint8_t *M0, *M1, *N0, *N1;
   int64_t m_batch, n_batch;  // bytes between matrices
+  int m_ld, n_ld;            // values per row
   int K;                     // reduction length (values), a multiple of 64
   int mt, nt;                // row and column tiles (symmetric products: mt == nt)
-  // results and the elementwise operand: hi and lo, [rows][ld]; the transposed result T0 (T1: SPLIT) [cols][ld_t]
+  // results and the elementwise operand, hi and lo, [rows][ld]; symmetric products also store the mirrored tile
   const uint8_t *E0, *E1;
-  uint8_t *R0, *R1, *T0, *T1;
-  int ld, ld_t;
-  int64_t r_batch, t_batch;  // bytes between matrices
-  float alpha, beta;         // result = alpha * E + beta * product
+  uint8_t *R0, *R1;
+  int ld;
+  int64_t r_batch;           // bytes between matrices
+  float alpha, beta, diag;   // result = alpha * E + beta * product + diag on the diagonal (POLY)
   // the first `whole` tiles are one workgroup each; `parts` workgroups share each of the rest
   int whole, parts;
   float* partial;            // [rest * parts][tile values]
-  // FINAL: out [m][n], row i of X is row i of out (flip: column i)
+  // FINAL: out [m][n]; turn: row i of the result is column i of out
   uint8_t* out;
   int m, n;
-  bool flip, out_bf16, out_vec;
+  bool turn, out_bf16, out_vec;
 };
 
 // fp16 pair of a value: hi = rounded, lo = the rest rounded
@@ -99,12 +100,36 @@ MOE_DEV void wave_lds_fence() {
   __builtin_amdgcn_wave_barrier();
 }
 
-// One stage with both operands as hi + lo: acc += lo hi + hi lo + hi hi.  The lo rows follow the hi rows of an operand at
-// a_lo / b_lo bytes.
+// ---------------------------------------------------------------------------------------------------------
+// Stages.  An operand whose reduction is contiguous (A, B, and X^T in B X) lies in a stage as B rows of RB bytes, in the
+// layout of the grouped products (gemm_tile.h).  X X^T reduces over the rows of X^T [Q][P]: a stage then holds RB / 2 of
+// those rows, B values of each, and the fragments are read with the transposing LDS load: 16 lanes read 4 rows x 16 values,
+// 8 bytes each, and lane l gets the 4 values of column l.  One such load of a wavefront covers rows k .. k + 3 and
+// k + 8 .. k + 11 of 32 columns; a row's 64-byte chunks (32 columns) are stored at chunk ^ (row & 3) (64-value rows:
+// chunk ^ (row / 2 & 1)), so that the four rows that are served together fall on distinct banks.
+// ---------------------------------------------------------------------------------------------------------
+typedef short i16x4_t __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) i16x4_t lds_i16x4_t;
+template <int B>
+MOE_DEV int swz_t(int row) {
+  return B >= 128 ? row & 3 : (row >> 1) & 1;
+}
+template <int ROWB>
+MOE_DEV f16x8_t frag_t(tile::lds_u8_t* p, int imm) {
+  union {
+    i16x4_t h[2];
+    f16x8_t f;
+  } u;
+  u.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t*)(p + imm));
+  u.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t*)(p + imm + 4 * ROWB));
+  return u.f;
+}
+
+// acc += the products of one stage; SPLIT: lo hi + hi lo + hi hi, the lo array of an operand ARR bytes behind its hi array.
+// ao, bo: byte offsets of this lane's fragments: per reduction step (rows of RB bytes) or per 32 columns (transposed).
 template <int RB, int MB, int NB>
-MOE_DEV void mma_stage_split(const uint8_t* As, const uint8_t* Bs, int a_lo, int b_lo, const int (&arow)[MB],
-                             const int (&brow)[NB], const tile::FragOff& ao, const tile::FragOff& bo,
-                             f32x16_t (&acc)[MB][NB]) {
+MOE_DEV void mma_stage_split(const uint8_t* As, const uint8_t* Bs, int ARR, const int (&arow)[MB], const int (&brow)[NB],
+                             const tile::FragOff& ao, const tile::FragOff& bo, f32x16_t (&acc)[MB][NB]) {
 #pragma unroll
   for (int s = 0; s < RB / 32; ++s) {
     tile::lds_u8_t* av = tile::to_lds(As) + ao.o[s];
@@ -113,18 +138,80 @@ MOE_DEV void mma_stage_split(const uint8_t* As, const uint8_t* Bs, int a_lo, int
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
       bh[j] = __builtin_bit_cast(f16x8_t, tile::lds_at(bv, (brow[j] - brow[0]) * RB));
-      bl[j] = __builtin_bit_cast(f16x8_t, tile::lds_at(bv, b_lo + (brow[j] - brow[0]) * RB));
+      bl[j] = __builtin_bit_cast(f16x8_t, tile::lds_at(bv, ARR + (brow[j] - brow[0]) * RB));
     }
 #pragma unroll
     for (int i = 0; i < MB; ++i) {
       const f16x8_t ah = __builtin_bit_cast(f16x8_t, tile::lds_at(av, (arow[i] - arow[0]) * RB));
-      const f16x8_t al = __builtin_bit_cast(f16x8_t, tile::lds_at(av, a_lo + (arow[i] - arow[0]) * RB));
+      const f16x8_t al = __builtin_bit_cast(f16x8_t, tile::lds_at(av, ARR + (arow[i] - arow[0]) * RB));
 #pragma unroll
       for (int j = 0; j < NB; ++j) acc[i][j] = mfma_32x32x16(al, bh[j], acc[i][j]);
 #pragma unroll
       for (int j = 0; j < NB; ++j) acc[i][j] = mfma_32x32x16(ah, bl[j], acc[i][j]);
 #pragma unroll
       for (int j = 0; j < NB; ++j) acc[i][j] = mfma_32x32x16(ah, bh[j], acc[i][j]);
+    }
+  }
+}
+
+template <int RB, int B, bool SPLIT, int MB, int NB>
+MOE_DEV void mma_stage_t(const uint8_t* As, const uint8_t* Bs, const uint32_t (&ao)[MB], const uint32_t (&bo)[NB],
+                         f32x16_t (&acc)[MB][NB]) {
+  constexpr int STEPS = RB / 32, ROWB = 2 * B, STEP = 16 * ROWB, ARR = B * RB;
+  tile::lds_u8_t *av[MB], *bv[NB];
+#pragma unroll
+  for (int i = 0; i < MB; ++i) av[i] = tile::to_lds(As) + ao[i];
+#pragma unroll
+  for (int j = 0; j < NB; ++j) bv[j] = tile::to_lds(Bs) + bo[j];
+  if constexpr (SPLIT) {
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+      f16x8_t bh[NB], bl[NB];
+#pragma unroll
+      for (int j = 0; j < NB; ++j) {
+        bh[j] = frag_t<ROWB>(bv[j], s * STEP);
+        bl[j] = frag_t<ROWB>(bv[j], ARR + s * STEP);
+      }
+#pragma unroll
+      for (int i = 0; i < MB; ++i) {
+        const f16x8_t ah = frag_t<ROWB>(av[i], s * STEP), al = frag_t<ROWB>(av[i], ARR + s * STEP);
+#pragma unroll
+        for (int j = 0; j < NB; ++j) acc[i][j] = mfma_32x32x16(al, bh[j], acc[i][j]);
+#pragma unroll
+        for (int j = 0; j < NB; ++j) acc[i][j] = mfma_32x32x16(ah, bl[j], acc[i][j]);
+#pragma unroll
+        for (int j = 0; j < NB; ++j) acc[i][j] = mfma_32x32x16(ah, bh[j], acc[i][j]);
+      }
+    }
+  } else {
+    // fragments double-buffered in registers: step s + 1's loads go between step s's products
+    f16x8_t fa[2][MB], fb[2][NB];
+#pragma unroll
+    for (int i = 0; i < MB; ++i) fa[0][i] = frag_t<ROWB>(av[i], 0);
+#pragma unroll
+    for (int j = 0; j < NB; ++j) fb[0][j] = frag_t<ROWB>(bv[j], 0);
+    sched_fence();
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+      const int c = s & 1;
+      if (s + 1 < STEPS) {
+#pragma unroll
+        for (int i = 0; i < MB; ++i) fa[c ^ 1][i] = frag_t<ROWB>(av[i], (s + 1) * STEP);
+#pragma unroll
+        for (int j = 0; j < NB; ++j) fb[c ^ 1][j] = frag_t<ROWB>(bv[j], (s + 1) * STEP);
+      }
+#pragma unroll
+      for (int i = 0; i < MB; ++i)
+#pragma unroll
+        for (int j = 0; j < NB; ++j) acc[i][j] = mfma_32x32x16(fa[c][i], fb[c][j], acc[i][j]);
+      if (s + 1 < STEPS) {
+#pragma unroll
+        for (int q = 0; q < MB + NB; ++q) {
+          __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        }
+      }
+      sched_fence();
     }
   }
 }
@@ -162,27 +249,27 @@ MOE_DEV TileAt tile_at(const Args& a, int L) {
 
 // What follows a product for one 32 x W block of a wavefront (W = WTN columns), through the wavefront's own LDS block, so
 // that every global access is 16 bytes per lane: by rows for the result (and the elementwise operand, loaded ahead by the
-// caller), by columns for the transpose.
+// caller), by columns for a transposed one.
 // Accumulator element v of a lane: row (v / 4) * 8 + 4 * (lane / 32) + v % 4, column lane % 32.
 template <int MODE, int W, bool SPLIT>
 struct Epilogue {
-  static constexpr bool SYM = MODE == GRAM || MODE == POLY;
-  static constexpr bool HAS_E = MODE != GRAM, E_LO = MODE == UPDATE || MODE == FINAL || (MODE == POLY && SPLIT);
+  static constexpr bool SYM = MODE == GRAM || MODE == POLY, FROM_X = MODE == UPDATE || MODE == FINAL;
+  // elementwise operand: A for B = b A + c A A; of X its lo part (hi comes with the product: B carries a on its diagonal,
+  // and with SPLIT the lo part does too)
+  static constexpr bool E_HI = MODE == POLY, E_LO = SPLIT ? MODE == POLY : FROM_X;
   static constexpr int NB = W / 32, PITCH = W + 4;                       // floats per row of the LDS block
   static constexpr int LPR = W / 8, RPP = 64 / LPR, PASS = 32 / RPP;     // lanes per row, rows per pass, passes
   struct Elem {
-    f16x8_t h[HAS_E ? PASS : 1], l[E_LO ? PASS : 1];
+    f16x8_t h[E_HI ? PASS : 1], l[E_LO ? PASS : 1];
   };
 
   static MOE_DEV void load(const Args& a, int e, int row0, int col0, Elem& x) {
-    if constexpr (HAS_E) {
-      const int lane = threadIdx.x & 63;
+    const int lane = threadIdx.x & 63;
 #pragma unroll
-      for (int it = 0; it < PASS; ++it) {
-        const int64_t at = e * a.r_batch + ((int64_t)(row0 + it * RPP + lane / LPR) * a.ld + col0 + lane % LPR * 8) * 2;
-        x.h[it] = *reinterpret_cast<const f16x8_t*>(a.E0 + at);
-        if constexpr (E_LO) x.l[it] = *reinterpret_cast<const f16x8_t*>(a.E1 + at);
-      }
+    for (int it = 0; it < PASS; ++it) {
+      const int64_t at = e * a.r_batch + ((int64_t)(row0 + it * RPP + lane / LPR) * a.ld + col0 + lane % LPR * 8) * 2;
+      if constexpr (E_HI) x.h[it] = *reinterpret_cast<const f16x8_t*>(a.E0 + at);
+      if constexpr (E_LO) x.l[it] = *reinterpret_cast<const f16x8_t*>(a.E1 + at);
     }
   }
 
@@ -210,7 +297,7 @@ struct Epilogue {
             (f32x4_t){v[4 * d], v[4 * d + 1], v[4 * d + 2], v[4 * d + 3]};
     }
   }
-  static MOE_DEV void store_pair(uint8_t* p0, uint8_t* p1, bool lo_too, int64_t at, const float (&v)[8]) {
+  static MOE_DEV void store_pair(const Args& a, int64_t at, const float (&v)[8]) {
     f16x8_t h, l;
 #pragma unroll
     for (int x = 0; x < 8; ++x) {
@@ -219,8 +306,8 @@ struct Epilogue {
       h[x] = hi;
       l[x] = lo;
     }
-    *reinterpret_cast<f16x8_t*>(p0 + at) = h;
-    if (lo_too) *reinterpret_cast<f16x8_t*>(p1 + at) = l;
+    *reinterpret_cast<f16x8_t*>(a.R0 + at) = h;
+    if constexpr (SPLIT || MODE == UPDATE) *reinterpret_cast<f16x8_t*>(a.R1 + at) = l;
   }
 
   // block at (row0, col0) of matrix e; mirror: also store it transposed
@@ -232,7 +319,7 @@ struct Epilogue {
 #pragma unroll
       for (int v = 0; v < 16; ++v) sc[((v >> 2) * 8 + 4 * lh + (v & 3)) * PITCH + j * 32 + lr] = acc[j][v];
     wave_lds_fence();
-    const bool turn = MODE == FINAL ? a.flip : mirror;
+    const bool turn = MODE == FINAL ? a.turn : SYM && mirror;
 #pragma unroll
     for (int it = 0; it < PASS; ++it) {
       const int r = it * RPP + lane / LPR, c = lane % LPR * 8;
@@ -243,17 +330,22 @@ struct Epilogue {
 #pragma unroll
         for (int x = 0; x < 4; ++x) v[4 * d + x] = a.beta * q[x];
       }
-      if constexpr (HAS_E) {
+      if constexpr (E_HI || E_LO) {
 #pragma unroll
         for (int x = 0; x < 8; ++x) {
-          float ev = (float)el.h[it][x];
+          float ev = 0.0f;
+          if constexpr (E_HI) ev += (float)el.h[it][x];
           if constexpr (E_LO) ev += (float)el.l[it][x];
           v[x] = __builtin_fmaf(a.alpha, ev, v[x]);
         }
       }
+      if constexpr (MODE == POLY) {
+#pragma unroll
+        for (int x = 0; x < 8; ++x) v[x] += row0 + r == col0 + c + x ? a.diag : 0.0f;
+      }
       if constexpr (MODE == FINAL) {
         const int gr = row0 + r, gc = col0 + c;
-        if (!a.flip && gr < a.m && gc < a.n) {
+        if (!turn && gr < a.m && gc < a.n) {
           const int64_t o = ((int64_t)e * a.m + gr) * a.n + gc;
           if (a.out_vec)  // n a multiple of 8: the 8 values are all inside, and aligned
             store_out8(a, o, v);
@@ -261,7 +353,7 @@ struct Epilogue {
             store_out(a, o, gc, v);
         }
       } else {
-        store_pair(a.R0, a.R1, MODE == UPDATE || SPLIT, e * a.r_batch + ((int64_t)(row0 + r) * a.ld + col0 + c) * 2, v);
+        store_pair(a, e * a.r_batch + ((int64_t)(row0 + r) * a.ld + col0 + c) * 2, v);
       }
       if (turn)
 #pragma unroll
@@ -277,8 +369,8 @@ struct Epilogue {
       float v[8];
 #pragma unroll
       for (int x = 0; x < 8; ++x) v[x] = sc[(r + x) * PITCH + c];
+      const int gr = col0 + c, gc = row0 + r;  // row and first column of what is stored
       if constexpr (MODE == FINAL) {
-        const int gr = col0 + c, gc = row0 + r;  // row and first column of out
         if (gr < a.m && gc < a.n) {
           const int64_t o = ((int64_t)e * a.m + gr) * a.n + gc;
           if (a.out_vec)
@@ -287,7 +379,7 @@ struct Epilogue {
             store_out(a, o, gc, v);
         }
       } else {
-        store_pair(a.T0, a.T1, SPLIT, e * a.t_batch + ((int64_t)(col0 + c) * a.ld_t + row0 + r) * 2, v);
+        store_pair(a, e * a.r_batch + ((int64_t)gr * a.ld + gc) * 2, v);
       }
     }
     wave_lds_fence();
@@ -307,7 +399,7 @@ __global__ __launch_bounds__((64 * Cfg<SIZE, SPLIT>::WM * Cfg<SIZE, SPLIT>::WN))
   using Epi = Epilogue<MODE, WTN, SPLIT>;
   constexpr int EPI = NW * 32 * Epi::PITCH * 4;
   constexpr int SMEM = NS * STAGE > EPI ? NS * STAGE : EPI;
-  constexpr bool SYM = Epi::SYM;
+  constexpr bool SYM = Epi::SYM, TR = MODE == GRAM;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[SMEM];
 
   const int lane = threadIdx.x & 63, wid = uniform_int(threadIdx.x >> 6);
@@ -325,12 +417,14 @@ __global__ __launch_bounds__((64 * Cfg<SIZE, SPLIT>::WM * Cfg<SIZE, SPLIT>::WN))
   }
   const TileAt at = tile_at<MODE>(a, L);
   const int e = at.e, m0 = at.mi * B, n0 = at.ni * B;
-  const int64_t Kb = (int64_t)a.K * 2;
-  const int nk_all = (int)(Kb / RB);
+  // this workgroup's stages, and a stage's step in memory (bytes)
+  const int nk_all = a.K * 2 / RB;
   const int k0 = uniform_int((int)((int64_t)nk_all * part / parts));
   const int nk = uniform_int((int)((int64_t)nk_all * (part + 1) / parts)) - k0;
-
-  const int64_t moff = e * a.m_batch + m0 * Kb + (int64_t)k0 * RB, noff = e * a.n_batch + n0 * Kb + (int64_t)k0 * RB;
+  const int64_t m_row = (int64_t)a.m_ld * 2, n_row = (int64_t)a.n_ld * 2;
+  const int64_t m_step = TR ? m_row * (RB / 2) : RB, n_step = TR ? n_row * (RB / 2) : RB;
+  const int64_t moff = e * a.m_batch + k0 * m_step + (TR ? m0 * 2 : m0 * m_row);
+  const int64_t noff = e * a.n_batch + k0 * n_step + (TR ? n0 * 2 : n0 * n_row);
   const uint8_t* base[NA];
   base[0] = uniform_ptr(a.M0 + moff);
   base[NA / 2] = uniform_ptr(a.N0 + noff);
@@ -338,18 +432,29 @@ __global__ __launch_bounds__((64 * Cfg<SIZE, SPLIT>::WM * Cfg<SIZE, SPLIT>::WN))
     base[1] = uniform_ptr(a.M1 + moff);
     base[3] = uniform_ptr(a.N1 + noff);
   }
-  uint32_t off[INS];
+  uint32_t m_off[INS], n_off[INS];
 #pragma unroll
   for (int q = 0; q < INS; ++q) {
-    const int r = (wid * INS + q) * RPI + lane / CPR;
-    off[q] = (uint32_t)(r * Kb + (((lane % CPR) ^ tile::swz<RB>(r)) << 4));
+    int r, at;  // row, and byte in it, of this lane's 16 bytes
+    if constexpr (TR) {
+      constexpr int PIECES = B / 8;
+      r = (wid * INS + q) * (64 / PIECES) + lane / PIECES;
+      const int piece = lane % PIECES;
+      at = (((piece / 4) ^ swz_t<B>(r)) * 4 + piece % 4) * 16;
+    } else {
+      r = (wid * INS + q) * RPI + lane / CPR;
+      at = ((lane % CPR) ^ tile::swz<RB>(r)) * 16;
+    }
+    m_off[q] = (uint32_t)(r * m_row + at);
+    n_off[q] = (uint32_t)(r * n_row + at);
   }
   auto load_stage = [&](uint8_t* dst, int kt) {
 #pragma unroll
     for (int x = 0; x < NA; ++x) {
-      const uint8_t* p = uniform_ptr(base[x] + (int64_t)kt * RB);
+      const uint8_t* p = uniform_ptr(base[x] + kt * (x < NA / 2 ? m_step : n_step));
 #pragma unroll
-      for (int q = 0; q < INS; ++q) load_lds16(p, off[q], dst + x * ARR + (wid * INS + q) * 1024);
+      for (int q = 0; q < INS; ++q)
+        load_lds16(p, x < NA / 2 ? m_off[q] : n_off[q], dst + x * ARR + (wid * INS + q) * 1024);
     }
   };
 
@@ -368,6 +473,15 @@ __global__ __launch_bounds__((64 * Cfg<SIZE, SPLIT>::WM * Cfg<SIZE, SPLIT>::WN))
   const tile::FragOff ao = tile::frag_offsets<RB, RB / 32>(arow[0], lh, 2);
   const tile::FragOff bo = tile::frag_offsets<RB, RB / 32>(brow[0], lh, 2);
 
+  uint32_t at_m[MB], at_n[NB];  // transposed fragments
+  {
+    const int k = (lane >> 5) * 8 + (lane >> 2 & 3), in = (lane >> 4 & 1) * 32 + (lane & 3) * 8;
+#pragma unroll
+    for (int i = 0; i < MB; ++i) at_m[i] = (uint32_t)(k * 2 * B + ((wm * MB + i) ^ swz_t<B>(k)) * 64 + in);
+#pragma unroll
+    for (int j = 0; j < NB; ++j) at_n[j] = (uint32_t)(k * 2 * B + ((wn * NB + j) ^ swz_t<B>(k)) * 64 + in);
+  }
+
   const int row0 = m0 + wm * WTM, col0 = n0 + wn * WTN;
   typename Epi::Elem el[2];
   if constexpr (SIZE == 0)
@@ -383,8 +497,10 @@ __global__ __launch_bounds__((64 * Cfg<SIZE, SPLIT>::WM * Cfg<SIZE, SPLIT>::WN))
     __syncthreads();
     load_stage(smem + fb * STAGE, min(kt + NS - 1, nk - 1));
     const uint8_t* As = smem + cb * STAGE;
-    if constexpr (SPLIT)
-      mma_stage_split<RB, MB, NB>(As, As + 2 * ARR, ARR, ARR, arow, brow, ao, bo, acc);
+    if constexpr (TR)
+      mma_stage_t<RB, B, SPLIT, MB, NB>(As, As + NA / 2 * ARR, at_m, at_n, acc);
+    else if constexpr (SPLIT)
+      mma_stage_split<RB, MB, NB>(As, As + 2 * ARR, ARR, arow, brow, ao, bo, acc);
     else
       tile::mma_stage_bf16<RB, MB, NB, f16x8_t>(As, As + ARR, arow, brow, ao, bo, acc);
     cb = cb + 1 == NS ? 0 : cb + 1;
@@ -409,7 +525,7 @@ __global__ __launch_bounds__((64 * Cfg<SIZE, SPLIT>::WM * Cfg<SIZE, SPLIT>::WN))
 
   // ---- epilogue, 32 rows at a time; the elementwise operand of a block is loaded while the block before is worked on (the
   // small tiles' before the product)
-  const bool mirror = MODE == UPDATE || (SYM && at.mi != at.ni);
+  const bool mirror = SYM && at.mi != at.ni;
   if constexpr (SIZE > 0) Epi::load(a, at.e, row0, col0, el[0]);
   wait_vmcnt0();
   __syncthreads();  // no load into LDS in flight, no wavefront still reading a stage: the epilogue reuses the buffers
@@ -450,7 +566,7 @@ __global__ __launch_bounds__(256) void join_kernel(const Args a) {
 #pragma unroll
         for (int v = 0; v < 4; ++v) acc[j][4 * q + v] += t[v];
       }
-  Epi::run(a, at.e, row0, col0, MODE == UPDATE || (Epi::SYM && at.mi != at.ni), acc, el, smem + w4 * 32 * Epi::PITCH);
+  Epi::run(a, at.e, row0, col0, Epi::SYM && at.mi != at.ni, acc, el, smem + w4 * 32 * Epi::PITCH);
 }
 
 MOE_DEV float load_g(const uint8_t* g, bool bf16, int64_t i) {
@@ -486,13 +602,13 @@ struct PrepArgs {
   const double* part;
   int chunks;
   float eps;
-  // natural (g's rows contiguous) and transposed destinations, either hi/lo; lo may be NULL
-  uint8_t *n0, *n1, *t0, *t1;
-  int ld_n, ld_t;    // values per row
+  bool turn;         // g's rows are the result's columns
+  uint8_t *y0, *y1;  // hi and lo
+  int ld;            // values per row
   int64_t batch_bytes;
 };
 
-// S g / (|g| + eps) as hi and lo, in both orientations, zero-filled past m x n
+// S g / (|g| + eps) as hi and lo, [Q][P], zero-filled past m x n
 __global__ __launch_bounds__(256) void prepare_kernel(const PrepArgs a) {
   __shared__ float t[64][65];
   __shared__ double red[4];
@@ -513,22 +629,21 @@ __global__ __launch_bounds__(256) void prepare_kernel(const PrepArgs a) {
   // the quotient in fp64: a gradient whose norm passes fp32's range, either way, still gives its X
   const double inv = (double)S / (sqrt(red[0] + red[1] + red[2] + red[3]) + (double)a.eps);
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {  // k < 2: rows of g, else columns; 8 values each
-    const int q = (k & 1) * 256 + tid, r = q / 8, c = q % 8 * 8;
+  for (int k = 0; k < 2; ++k) {  // 8 values of a row of the result each
+    const int q = k * 256 + tid, r = q / 8, c = q % 8 * 8;
     f16x8_t h, l;
 #pragma unroll
     for (int x = 0; x < 8; ++x) {
-      const float v = (float)((double)(k < 2 ? t[r][c + x] : t[c + x][r]) * inv);
+      const float v = (float)((double)(a.turn ? t[c + x][r] : t[r][c + x]) * inv);
       _Float16 hi, lo;
       split16(v, hi, lo);
       h[x] = hi;
       l[x] = lo;
     }
-    uint8_t *d0 = k < 2 ? a.n0 : a.t0, *d1 = k < 2 ? a.n1 : a.t1;
     const int64_t at = e * a.batch_bytes +
-                       (k < 2 ? (int64_t)(r0 + r) * a.ld_n + c0 + c : (int64_t)(c0 + r) * a.ld_t + r0 + c) * 2;
-    *reinterpret_cast<f16x8_t*>(d0 + at) = h;
-    if (d1 != nullptr) *reinterpret_cast<f16x8_t*>(d1 + at) = l;
+                       (a.turn ? (int64_t)(c0 + r) * a.ld + r0 + c : (int64_t)(r0 + r) * a.ld + c0 + c) * 2;
+    *reinterpret_cast<f16x8_t*>(a.y0 + at) = h;
+    *reinterpret_cast<f16x8_t*>(a.y1 + at) = l;
   }
 }
 
@@ -606,7 +721,7 @@ static Plan plan(int64_t batch, int m, int n, bool split) {
   z.Q = (z.q + tl - 1) / tl * tl;
   z.gram = shape(batch, z.P, z.P, z.Q, true, most, split);
   z.poly = shape(batch, z.P, z.P, z.P, true, most, split);
-  z.update = shape(batch, z.P, z.Q, z.P, false, most, split);
+  z.update = shape(batch, z.Q, z.P, z.P, false, most, split);
   const int64_t count = (int64_t)m * n;
   z.chunks = (int)(count / 4096 < 1 ? 1 : count / 4096 > 256 ? 256 : count / 4096);
   z.x_bytes = (size_t)batch * z.P * z.Q * 2;
@@ -614,7 +729,7 @@ static Plan plan(int64_t batch, int m, int n, bool split) {
   z.part_bytes = up256((size_t)batch * z.chunks * sizeof(double));
   for (const Shape* t : {&z.gram, &z.poly, &z.update})
     if (partial_bytes(*t) > z.partial) z.partial = partial_bytes(*t);
-  z.total = z.part_bytes + z.partial + (split ? 6 : 4) * z.x_bytes +
+  z.total = z.part_bytes + z.partial + (split ? 4 : 3) * z.x_bytes +
             (split ? 4 : 2) * z.a_bytes;
   return z;
 }
@@ -656,12 +771,11 @@ static void run(const OrthLaunch& p, hipStream_t s) {
   };
   double* part = reinterpret_cast<double*>(take(z.part_bytes));
   float* partial = reinterpret_cast<float*>(take(z.partial));
-  uint8_t *x0 = take(z.x_bytes), *x1 = take(z.x_bytes);
-  uint8_t *t0[2] = {take(z.x_bytes), take(z.x_bytes)}, *t1[2] = {nullptr, nullptr};
+  uint8_t *y0[2] = {take(z.x_bytes), take(z.x_bytes)}, *y1[2];
+  y1[0] = take(z.x_bytes);
+  y1[1] = SPLIT ? take(z.x_bytes) : y1[0];  // not an operand without SPLIT: updated in place
   uint8_t *a0 = take(z.a_bytes), *b0 = take(z.a_bytes), *a1 = nullptr, *b1 = nullptr;
   if constexpr (SPLIT) {
-    t1[0] = take(z.x_bytes);
-    t1[1] = take(z.x_bytes);
     a1 = take(z.a_bytes);
     b1 = take(z.a_bytes);
   }
@@ -678,12 +792,10 @@ static void run(const OrthLaunch& p, hipStream_t s) {
   r.part = part;
   r.chunks = z.chunks;
   r.eps = p.eps;
-  r.n0 = z.flip ? t0[0] : x0;
-  r.n1 = z.flip ? t1[0] : x1;
-  r.t0 = z.flip ? x0 : t0[0];
-  r.t1 = z.flip ? x1 : t1[0];
-  r.ld_n = z.flip ? z.P : z.Q;
-  r.ld_t = z.flip ? z.Q : z.P;
+  r.turn = !z.flip;
+  r.y0 = y0[0];
+  r.y1 = y1[0];
+  r.ld = z.P;
   r.batch_bytes = (int64_t)z.P * z.Q * 2;
   hipLaunchKernelGGL(prepare_kernel, dim3((unsigned)(p.batch * r.rt * r.ct)), dim3(256), 0, s, r);
 
@@ -692,51 +804,50 @@ static void run(const OrthLaunch& p, hipStream_t s) {
     const int cur = k & 1, nxt = cur ^ 1;
     Args q{};
     q.partial = partial;
-    q.M0 = q.N0 = x0;  // A = X X^T
-    q.M1 = q.N1 = x1;
+    q.M0 = q.N0 = y0[cur];  // A = X X^T
+    q.M1 = q.N1 = y1[cur];
     q.m_batch = q.n_batch = xb;
+    q.m_ld = q.n_ld = z.P;
     q.K = z.Q;
-    q.R0 = q.T0 = a0;
-    q.R1 = q.T1 = a1;
-    q.ld = q.ld_t = z.P;
-    q.r_batch = q.t_batch = ab;
+    q.R0 = a0;
+    q.R1 = a1;
+    q.ld = z.P;
+    q.r_batch = ab;
     q.beta = 1.0f / S;
     launch_product<GRAM, SPLIT>(q, z.gram, z.P, z.P, s);
-    q.M0 = q.N0 = q.E0 = a0;  // B = b A + c A A
+    q.M0 = q.N0 = q.E0 = a0;  // B = a + b A + c A A
     q.M1 = q.N1 = q.E1 = a1;
     q.m_batch = q.n_batch = ab;
     q.K = z.P;
-    q.R0 = q.T0 = b0;
-    q.R1 = q.T1 = b1;
+    q.R0 = b0;
+    q.R1 = b1;
     q.alpha = p.b;
     q.beta = p.c / S;
+    q.diag = p.a * S;
     launch_product<POLY, SPLIT>(q, z.poly, z.P, z.P, s);
-    q.M0 = b0;  // X <- a X + B X
-    q.M1 = b1;
-    q.N0 = t0[cur];
-    q.N1 = t1[cur];
-    q.n_batch = xb;
-    q.E0 = q.R0 = x0;
-    q.E1 = q.R1 = x1;
-    q.ld = z.Q;
-    q.r_batch = q.t_batch = xb;
-    q.T0 = t0[nxt];
-    q.T1 = t1[nxt];
-    q.ld_t = z.P;
-    q.alpha = p.a;
-    q.beta = 1.0f / S;
+    q.M0 = y0[cur];  // X^T <- X^T B
+    q.M1 = y1[cur];
+    q.m_batch = xb;
+    q.N0 = b0;
+    q.N1 = b1;
+    q.E1 = y1[cur];
+    q.R0 = y0[nxt];
+    q.R1 = y1[nxt];
+    q.r_batch = xb;
     if (k + 1 < p.steps) {
-      launch_product<UPDATE, SPLIT>(q, z.update, z.P, z.Q, s);
+      q.alpha = p.a;
+      q.beta = 1.0f / S;
+      launch_product<UPDATE, SPLIT>(q, z.update, z.Q, z.P, s);
     } else {
       q.alpha = p.a * (p.scale / S);
       q.beta = p.scale / S / S;
       q.out = reinterpret_cast<uint8_t*>(p.out);
       q.m = p.m;
       q.n = p.n;
-      q.flip = z.flip;
+      q.turn = !z.flip;
       q.out_bf16 = p.out_bf16;
       q.out_vec = p.n % 8 == 0 && (uintptr_t)p.out % 16 == 0;
-      launch_product<FINAL, SPLIT>(q, z.update, z.P, z.Q, s);
+      launch_product<FINAL, SPLIT>(q, z.update, z.Q, z.P, s);
     }
   }
 }

@@ -423,7 +423,7 @@ moe_status moe_norm_backward(const void* dy, int64_t ld_dy, const void* s, int64
  *   X's values are held to 2^-37 at least: a g whose norm is below about 1e-9 eps gives zeros.
  *   workspace (device) at least moe_orthogonalize_workspace_bytes(batch, m, n, out_dtype) bytes, 256-byte aligned.
  * Domain: batch >= 0, 1 <= m, n <= 65536, 1 <= steps <= 32, eps > 0 and finite, scale finite, and coefficients that keep
- * the iteration bounded: from singular values in [0, 1] every step's stay within 3, and those of b A + c A A within 12
+ * the iteration bounded: from singular values in [0, 1] every step's stay within 3, and those of a + b A + c A A within 12
  * (MOE_ERR_INVALID_ARG otherwise).  Results do not depend on run or launch order.
  */
 size_t moe_orthogonalize_workspace_bytes(int64_t batch, int32_t m, int32_t n, moe_dtype out_dtype);
