@@ -569,27 +569,63 @@ __global__ __launch_bounds__(256) void join_kernel(const Args a) {
   Epi::run(a, at.e, row0, col0, Epi::SYM && at.mi != at.ni, acc, el, smem + w4 * 32 * Epi::PITCH);
 }
 
-MOE_DEV float load_g(const uint8_t* g, bool bf16, int64_t i) {
-  if (bf16) return __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(g)[i] << 16);
-  return reinterpret_cast<const float*>(g)[i];
+// Four consecutive values of g from index i on, at the elements' own alignment (one wide access), zeros from `end` on
+typedef float f32x4_e4_t __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint16_t u16x4_e2_t __attribute__((ext_vector_type(4), aligned(2)));
+MOE_DEV f32x4_t load_g4(const uint8_t* g, bool bf16, int64_t i, int64_t end) {
+  f32x4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (bf16) {
+    const uint16_t* p = reinterpret_cast<const uint16_t*>(g) + i;
+    if (i + 4 <= end) {
+      const u16x4_e2_t q = *reinterpret_cast<const u16x4_e2_t*>(p);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) v[x] = __uint_as_float((uint32_t)q[x] << 16);
+    } else {
+#pragma unroll
+      for (int x = 0; x < 3; ++x)
+        if (i + x < end) v[x] = __uint_as_float((uint32_t)p[x] << 16);
+    }
+  } else {
+    const float* p = reinterpret_cast<const float*>(g) + i;
+    if (i + 4 <= end) {
+      v = *reinterpret_cast<const f32x4_e4_t*>(p);
+    } else {
+#pragma unroll
+      for (int x = 0; x < 3; ++x)
+        if (i + x < end) v[x] = p[x];
+    }
+  }
+  return v;
 }
 
-// part[e][chunk] = sum of the squares of the chunk's values, in fp64 (squares of fp32 values neither overflow nor vanish)
+// part[e][chunk] = sum of the squares of the chunk's values, in fp64 (squares of fp32 values neither overflow nor vanish);
+// `step` values per chunk, a multiple of 4
 __global__ __launch_bounds__(256) void square_sum_kernel(const uint8_t* __restrict__ g, bool bf16, int64_t count,
-                                                         int chunks, double* __restrict__ part) {
+                                                         int64_t step, int chunks, double* __restrict__ part) {
   __shared__ double red[4];
   const int64_t e = blockIdx.x / chunks;
-  const int ch = blockIdx.x % chunks;
-  const int64_t step = (count + chunks - 1) / chunks, lo = ch * step, hi = lo + step < count ? lo + step : count;
-  const int64_t base = e * count;
-  double s = 0.0;
-  for (int64_t i = lo + threadIdx.x; i < hi; i += 256) {
-    const double v = load_g(g, bf16, base + i);
-    s = __builtin_fma(v, v, s);
-  }
+  const int64_t lo = blockIdx.x % chunks * step, hi = lo + step < count ? lo + step : count;
+  const int64_t base = e * count, end = base + hi;
+  double s[4] = {0.0, 0.0, 0.0, 0.0};
+  int64_t i = base + lo + threadIdx.x * 4;
+  for (; i + 3 * 1024 + 4 <= end; i += 4 * 1024) {  // four loads in flight
+    f32x4_t v[4];
 #pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) s += __shfl_xor(s, o, 64);
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
+    for (int u = 0; u < 4; ++u) v[u] = load_g4(g, bf16, i + u * 1024, end);
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) s[x] = __builtin_fma((double)v[u][x], (double)v[u][x], s[x]);
+  }
+  for (; i < end; i += 1024) {
+    const f32x4_t v = load_g4(g, bf16, i, end);
+#pragma unroll
+    for (int x = 0; x < 4; ++x) s[x] = __builtin_fma((double)v[x], (double)v[x], s[x]);
+  }
+  double t = (s[0] + s[1]) + (s[2] + s[3]);
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) t += __shfl_xor(t, o, 64);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = t;
   __syncthreads();
   if (threadIdx.x == 0) part[blockIdx.x] = red[0] + red[1] + red[2] + red[3];
 }
@@ -621,20 +657,28 @@ __global__ __launch_bounds__(256) void prepare_kernel(const PrepArgs a) {
   for (int o = 32; o >= 1; o >>= 1) s += __shfl_xor(s, o, 64);
   if ((tid & 63) == 0) red[tid >> 6] = s;
 #pragma unroll
-  for (int k = 0; k < 16; ++k) {
-    const int r = k * 4 + tid / 64, c = tid % 64;
-    t[r][c] = r0 + r < a.m && c0 + c < a.n ? load_g(a.g, a.bf16, (e * a.m + r0 + r) * a.n + c0 + c) : 0.0f;
+  for (int k = 0; k < 4; ++k) {
+    const int r = k * 16 + tid / 16, c = tid % 16 * 4;
+    f32x4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (r0 + r < a.m && c0 + c < a.n) {
+      const int64_t row = (e * a.m + r0 + r) * a.n;
+      v = load_g4(a.g, a.bf16, row + c0 + c, row + a.n);
+    }
+#pragma unroll
+    for (int x = 0; x < 4; ++x) t[r][c + x] = v[x];
   }
   __syncthreads();
-  // the quotient in fp64: a gradient whose norm passes fp32's range, either way, still gives its X
-  const double inv = (double)S / (sqrt(red[0] + red[1] + red[2] + red[3]) + (double)a.eps);
+  // The quotient as a fraction in [1/2, 1) and a power of two, so that a gradient whose norm passes fp32's range, either
+  // way, still gives its X; the fraction's rounding to fp32 is below the 22 bits that X keeps.
+  int power;
+  const float fraction = (float)frexp((double)S / (sqrt(red[0] + red[1] + red[2] + red[3]) + (double)a.eps), &power);
 #pragma unroll
   for (int k = 0; k < 2; ++k) {  // 8 values of a row of the result each
     const int q = k * 256 + tid, r = q / 8, c = q % 8 * 8;
     f16x8_t h, l;
 #pragma unroll
     for (int x = 0; x < 8; ++x) {
-      const float v = (float)((double)(a.turn ? t[c + x][r] : t[r][c + x]) * inv);
+      const float v = ldexpf((a.turn ? t[c + x][r] : t[r][c + x]) * fraction, power);
       _Float16 hi, lo;
       split16(v, hi, lo);
       h[x] = hi;
@@ -657,11 +701,11 @@ struct Shape {
 
 // Microseconds of a product, to choose by: a launch of its own, then for every 256 tiles (one per compute unit; two smaller
 // tiles that share one take as long as one after the other) the reduction and the epilogue.  Measured on kernels of 24 to
-// 8192 tiles, K = 512 to 14336; one 256 x 256 tile holds 16 of 64 x 64, so per value the sizes cost 25 : 37 : 67.
+// 8192 tiles, K = 512 to 14336; one 256 x 256 tile holds 16 of 64 x 64, so per value the sizes cost 22 : 37 : 67.
 //                               64 x 64        128 x 128      256 x 256
-constexpr double PER_K[2][3] = {{4.2e-3, 9.2e-3, 25e-3}, {8.5e-3, 27e-3, 72e-3}};  // [SPLIT]
+constexpr double PER_K[2][3] = {{4.2e-3, 9.2e-3, 22e-3}, {8.5e-3, 27e-3, 72e-3}};  // [SPLIT]
 constexpr double EPI_SYM[2][3] = {{1.0, 4.0, 10.0}, {1.5, 6.0, 15.0}};
-constexpr double EPI_UPDATE[2][3] = {{1.0, 5.0, 33.0}, {1.5, 7.0, 50.0}};
+constexpr double EPI_UPDATE[2][3] = {{1.0, 5.0, 19.0}, {1.5, 7.0, 28.0}};
 constexpr double LAUNCH_US = 4.5, BYTES_PER_US = 4e6;
 
 static Shape shape(int64_t batch, int rows, int cols, int K, bool sym, int most_size, bool split) {
@@ -701,6 +745,7 @@ struct Plan {
   int p, q, P, Q;
   bool flip;
   int chunks;
+  int64_t chunk_values;
   Shape gram, poly, update;
   size_t x_bytes, a_bytes;  // one fp16 array of the whole batch
   size_t part_bytes, partial, total;
@@ -723,7 +768,9 @@ static Plan plan(int64_t batch, int m, int n, bool split) {
   z.poly = shape(batch, z.P, z.P, z.P, true, most, split);
   z.update = shape(batch, z.Q, z.P, z.P, false, most, split);
   const int64_t count = (int64_t)m * n;
+  // chunks of 4096 values or more, 256 at most: a workgroup of the next kernel adds one per thread
   z.chunks = (int)(count / 4096 < 1 ? 1 : count / 4096 > 256 ? 256 : count / 4096);
+  z.chunk_values = ((count + z.chunks - 1) / z.chunks + 3) / 4 * 4;
   z.x_bytes = (size_t)batch * z.P * z.Q * 2;
   z.a_bytes = (size_t)batch * z.P * z.P * 2;
   z.part_bytes = up256((size_t)batch * z.chunks * sizeof(double));
@@ -781,7 +828,7 @@ static void run(const OrthLaunch& p, hipStream_t s) {
   }
   const uint8_t* g = reinterpret_cast<const uint8_t*>(p.g);
   hipLaunchKernelGGL(square_sum_kernel, dim3((unsigned)(p.batch * z.chunks)), dim3(256), 0, s, g, p.g_bf16,
-                     (int64_t)p.m * p.n, z.chunks, part);
+                     (int64_t)p.m * p.n, z.chunk_values, z.chunks, part);
   PrepArgs r{};
   r.g = g;
   r.bf16 = p.g_bf16;
