@@ -132,9 +132,9 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-def _stream(stream):
+def _stream(stream, index=None):
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if index is None else index)
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
@@ -464,7 +464,7 @@ def _on_device(fn, dev, stream):
     """Context of a call on tensors of device ``dev``: kernels are launched with that device current."""
     if dev.type != "cuda":
         raise ValueError(f"{fn}: tensors must be on the GPU (got {dev})")
-    if isinstance(stream, torch.cuda.Stream) and stream.device != dev:
+    if stream is not None and isinstance(stream, torch.cuda.Stream) and stream.device != dev:
         raise ValueError(f"{fn}: the stream is on {stream.device}, the tensors on {dev}")
     return _CURRENT if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
 
@@ -472,27 +472,26 @@ def _on_device(fn, dev, stream):
 def _tensor(fn, name, t, shape, dtypes, index):
     """Checks one contiguous tensor argument on GPU ``index`` (-1: the CPU) against what the C call assumes of its
     pointer; returns the pointer."""
+    if t.is_contiguous() and t.shape == shape and t.dtype in dtypes and t.get_device() == index:
+        return t.data_ptr()
+    _refuse(fn, name, t, shape, dtypes, index)
+    raise ValueError(f"{fn}: {name} must be contiguous")
+
+
+def _refuse(fn, name, t, shape, dtypes, index):
     if t.shape != shape:
         raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, not {tuple(shape)}")
     if t.dtype not in dtypes:
         raise ValueError(f"{fn}: {name} has dtype {t.dtype}, not {' or '.join(map(str, dtypes))}")
     if t.get_device() != index:
         raise ValueError(f"{fn}: {name} is on {t.device}, the rows or matrices are not")
-    if not t.is_contiguous():
-        raise ValueError(f"{fn}: {name} must be contiguous")
-    return t.data_ptr()
 
 
 def _rows(fn, name, t, shape, dtype, index):
     """Checks rows whose values are contiguous and whose stride is free; returns the pointer and the stride in elements."""
-    if t.is_contiguous():
-        return _tensor(fn, name, t, shape, (dtype,), index), shape[1]
-    if t.shape != shape:
-        raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, not {tuple(shape)}")
-    if t.dtype != dtype:
-        raise ValueError(f"{fn}: {name} has dtype {t.dtype}, not {dtype}")
-    if t.get_device() != index:
-        raise ValueError(f"{fn}: {name} is on {t.device}, the rows are not")
+    if t.is_contiguous() and t.shape == shape and t.dtype is dtype and t.get_device() == index:
+        return t.data_ptr(), shape[1]
+    _refuse(fn, name, t, shape, (dtype,), index)
     T, H = shape
     if H > 1 and t.stride(1) != 1:
         raise ValueError(f"{fn}: {name}'s rows must be contiguous")
@@ -504,6 +503,8 @@ def _rows(fn, name, t, shape, dtype, index):
 _ROW_TYPES = (torch.float32, torch.bfloat16)
 _FP8_TYPES = (torch.uint8, torch.float8_e4m3fn)
 _F32 = (torch.float32,)
+_CODES = {torch.float32: MOE_DTYPE_F32, torch.bfloat16: MOE_DTYPE_BF16, torch.uint8: MOE_DTYPE_FP8_E4M3,
+          torch.float8_e4m3fn: MOE_DTYPE_FP8_E4M3}
 
 
 @dataclasses.dataclass
@@ -516,14 +517,16 @@ class Norm:
 
 
 def _norm_args(fn, x, weight, kind):
-    if kind not in NORM_KINDS:
+    code = NORM_KINDS.get(kind)
+    if code is None:
         raise ValueError(f"{fn}: kind {kind!r} is not one of {tuple(NORM_KINDS)}")
-    if x.dim() != 2:
-        raise ValueError(f"{fn}: rows must be [T, H] (got {tuple(x.shape)})")
-    if x.dtype not in _ROW_TYPES:
-        raise ValueError(f"{fn}: rows must be float32 or bfloat16 (got {x.dtype})")
+    shape, dt = x.shape, x.dtype
+    if len(shape) != 2:
+        raise ValueError(f"{fn}: rows must be [T, H] (got {tuple(shape)})")
+    if dt not in _ROW_TYPES:
+        raise ValueError(f"{fn}: rows must be float32 or bfloat16 (got {dt})")
     index = x.get_device()
-    return x.shape, index, _tensor(fn, "weight", weight, x.shape[1:], _ROW_TYPES, index)
+    return shape, dt, index, code, _tensor(fn, "weight", weight, shape[1:], _ROW_TYPES, index)
 
 
 def moe_norm(x, weight, bias=None, residual=None, kind="layer", eps=1e-5, out_dtype=None, y=None, y_scales=None,
@@ -534,21 +537,20 @@ def moe_norm(x, weight, bias=None, residual=None, kind="layer", eps=1e-5, out_dt
     out_dtype: x's (default), or torch.float8_e4m3fn / torch.uint8: e4m3 codes with y_scales [T, H/128], as
     moe_dispatch_permute takes them.  ``sum`` may be x or residual themselves."""
     fn = "moe_norm"
-    shape, index, w_ptr = _norm_args(fn, x, weight, kind)
+    shape, dt, index, kind, w_ptr = _norm_args(fn, x, weight, kind)
     T, H = shape
-    dt = x.dtype
     x_ptr, ldx = _rows(fn, "x", x, shape, dt, index)
     r_ptr, ldr = (None, 0) if residual is None else _rows(fn, "residual", residual, shape, dt, index)
     b_ptr = None if bias is None else _tensor(fn, "bias", bias, weight.shape, (weight.dtype,), index)
     if y is not None and out_dtype is not None and y.dtype != out_dtype:
         raise ValueError(f"{fn}: y has dtype {y.dtype}, not {out_dtype}")
     yt = y.dtype if y is not None else out_dtype or dt
-    fp8 = yt in _FP8_TYPES
-    if not fp8 and yt != dt:
+    fp8 = yt is not dt
+    if fp8 and yt not in _FP8_TYPES:
         raise NotImplementedError(f"{fn}: the output is the rows' dtype or e4m3 codes, not {yt}")
     if fp8 and H % 128:
         raise ValueError(f"{fn}: e4m3 rows need H = {H} to be a multiple of 128")
-    layer = kind == "layer"
+    layer = kind == MOE_NORM_LAYER
     with _on_device(fn, x.device, stream):
         if (y is None or rstd is None or (fp8 and y_scales is None) or (layer and mean is None)
                 or (residual is not None and sum is None)):
@@ -569,9 +571,10 @@ def moe_norm(x, weight, bias=None, residual=None, kind="layer", eps=1e-5, out_dt
         ys_ptr = _tensor(fn, "y_scales", y_scales, (T, H // 128), _F32, index) if fp8 else None
         mean_ptr = _tensor(fn, "mean", mean, shape[:1], _F32, index) if layer else None
         sum_ptr = None if residual is None else _tensor(fn, "sum", sum, shape, (dt,), index)
-        _check(lib.moe_norm(x_ptr, ldx, r_ptr, ldr, dtype_code(dt), T, H, NORM_KINDS[kind], w_ptr, b_ptr,
-                            dtype_code(weight.dtype), eps, sum_ptr, y_ptr, ys_ptr, dtype_code(yt), mean_ptr, rstd_ptr,
-                            _stream(stream)), fn)
+        st = lib.moe_norm(x_ptr, ldx, r_ptr, ldr, _CODES[dt], T, H, kind, w_ptr, b_ptr, _CODES[weight.dtype], eps,
+                          sum_ptr, y_ptr, ys_ptr, _CODES[yt], mean_ptr, rstd_ptr, _stream(stream, index))
+    if st:
+        _check(st, fn)
     return Norm(y, y_scales if fp8 else None, x if residual is None else sum, mean if layer else None, rstd)
 
 
@@ -587,10 +590,9 @@ def moe_norm_backward(dy, rows, weight, mean, rstd, kind="layer", dsum=None, wan
     residual stream) added.  dx may be dy or dsum themselves (out["dx"]).  want_bias: default, for kind "layer" only
     (with ``out``: where out["dbias"] is given)."""
     fn = "moe_norm_backward"
-    shape, index, w_ptr = _norm_args(fn, rows, weight, kind)
+    shape, dt, index, kind, w_ptr = _norm_args(fn, rows, weight, kind)
     T, H = shape
-    dt = rows.dtype
-    layer = kind == "layer"
+    layer = kind == MOE_NORM_LAYER
     if want_bias is None:
         want_bias = layer if out is None else out.get("dbias") is not None
     s_ptr, ld_s = _rows(fn, "rows", rows, shape, dt, index)
@@ -615,21 +617,20 @@ def moe_norm_backward(dy, rows, weight, mean, rstd, kind="layer", dsum=None, wan
         if want_bias and out.get("dbias") is None:
             raise ValueError(f"{fn}: want_bias needs out['dbias']")
         db_ptr = _tensor(fn, "dbias", out["dbias"], shape[1:], _F32, index) if want_bias else None
-        _check(lib.moe_norm_backward(dy_ptr, ld_dy, s_ptr, ld_s, ds_ptr, ld_ds, dtype_code(dt), T, H, NORM_KINDS[kind],
-                                     w_ptr, dtype_code(weight.dtype), mean_ptr, rstd_ptr, dx_ptr, dw_ptr, db_ptr,
-                                     *_workspace(fn, workspace, index), _stream(stream)), fn)
+        ws_ptr, ws_bytes = _workspace(fn, workspace, index)
+        st = lib.moe_norm_backward(dy_ptr, ld_dy, s_ptr, ld_s, ds_ptr, ld_ds, _CODES[dt], T, H, kind, w_ptr,
+                                   _CODES[weight.dtype], mean_ptr, rstd_ptr, dx_ptr, dw_ptr, db_ptr, ws_ptr, ws_bytes,
+                                   _stream(stream, index))
+    if st:
+        _check(st, fn)
     return out
-
-
-def _nbytes(t) -> int:
-    return t.numel() * t.element_size()
 
 
 def _workspace(fn, t, index):
     """Pointer and size of a workspace tensor."""
     if t.get_device() != index or not t.is_contiguous():
         raise ValueError(f"{fn}: the workspace must be contiguous and on the GPU of the other tensors")
-    return t.data_ptr(), _nbytes(t)
+    return t.data_ptr(), t.nbytes
 
 
 # singular values 0.003 .. 1 come out between 0.68 and 1.21 after five steps
@@ -669,10 +670,10 @@ def moe_orthogonalize(g, steps=5, coeffs=ORTHOGONALIZE_COEFFS, eps=1e-7, scale=1
                     workspace = torch.empty(moe_orthogonalize_workspace_bytes(B, m, n, ot), dtype=torch.uint8,
                                             device=g.device)
         out_ptr = _tensor(fn, "out", out, g.shape, (ot,), index)
-        if g_ptr < out_ptr + _nbytes(out) and out_ptr < g_ptr + _nbytes(g):
+        if g_ptr < out_ptr + out.nbytes and out_ptr < g_ptr + g.nbytes:
             raise ValueError(f"{fn}: out must not overlap g")
         _check(lib.moe_orthogonalize(g_ptr, dtype_code(g.dtype), B, m, n, steps, *coeffs, eps, scale, out_ptr,
-                                     dtype_code(ot), *_workspace(fn, workspace, index), _stream(stream)), fn)
+                                     dtype_code(ot), *_workspace(fn, workspace, index), _stream(stream, index)), fn)
     return out
 
 
