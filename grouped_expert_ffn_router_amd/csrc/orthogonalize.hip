@@ -16,9 +16,10 @@
 // a^steps (485 for the usual coefficients), and with X rounded to 11 bits each step it would magnify that rounding with
 // them (a gradient of rank 1 then comes out 15% wrong, of rank 16 4%; measured in fp64 models of both).  Rounding the
 // operands of the products does not have this effect: an error in A or B multiplies X from the left, and leaves its row
-// space alone.
-// SPLIT (fp32 outputs) gives hi and lo to the operands too and sums lo hi + hi lo + hi hi: three passes over the reduction
-// with the same tiles.
+// space alone.  The last step, which magnifies by a alone, does without lo (bf16 results of 256 x 896 in the model: 2.15e-3
+// of the norm off for 2.19e-3 with lo, at rank 3 2.45e-3 for 2.24e-3; a rounding to bf16 is 1.7e-3).
+// SPLIT (fp32 outputs, and bf16 outputs of matrices so small that the launches are what is paid for) gives hi and lo to the
+// operands too and sums lo hi + hi lo + hi hi: three products, the same tiles.
 //
 // Layout: X [P][Q] hi and lo, its transpose [Q][P] (two, used in turn: a step's tiles read one and write the other), A and
 // B [P][P]; P and Q are p and q rounded up to the tile size and zero-filled, which the iteration keeps, so no product has
@@ -253,10 +254,10 @@ MOE_DEV TileAt tile_at(const Args& a, int L) {
 // Accumulator element v of a lane: row (v / 4) * 8 + 4 * (lane / 32) + v % 4, column lane % 32.
 template <int MODE, int W, bool SPLIT>
 struct Epilogue {
-  static constexpr bool SYM = MODE == GRAM || MODE == POLY, FROM_X = MODE == UPDATE || MODE == FINAL;
-  // elementwise operand: A for B = b A + c A A; of X its lo part (hi comes with the product: B carries a on its diagonal,
-  // and with SPLIT the lo part does too)
-  static constexpr bool E_HI = MODE == POLY, E_LO = SPLIT ? MODE == POLY : FROM_X;
+  static constexpr bool SYM = MODE == GRAM || MODE == POLY;
+  // elementwise operand: A for B = b A + c A A; of X its lo part, but in the last step (hi comes with the product: B carries
+  // a on its diagonal, and with SPLIT the lo part does too)
+  static constexpr bool E_HI = MODE == POLY, E_LO = SPLIT ? MODE == POLY : MODE == UPDATE;
   static constexpr int NB = W / 32, PITCH = W + 4;                       // floats per row of the LDS block
   static constexpr int LPR = W / 8, RPP = 64 / LPR, PASS = 32 / RPP;     // lanes per row, rows per pass, passes
   struct Elem {
@@ -307,7 +308,10 @@ struct Epilogue {
       l[x] = lo;
     }
     *reinterpret_cast<f16x8_t*>(a.R0 + at) = h;
-    if constexpr (SPLIT || MODE == UPDATE) *reinterpret_cast<f16x8_t*>(a.R1 + at) = l;
+    if constexpr (SPLIT)
+      *reinterpret_cast<f16x8_t*>(a.R1 + at) = l;
+    else if (MODE == UPDATE && a.R1 != nullptr)
+      *reinterpret_cast<f16x8_t*>(a.R1 + at) = l;
   }
 
   // block at (row0, col0) of matrix e; mirror: also store it transposed
@@ -569,6 +573,117 @@ __global__ __launch_bounds__(256) void join_kernel(const Args a) {
   Epi::run(a, at.e, row0, col0, Epi::SYM && at.mi != at.ni, acc, el, smem + w4 * 32 * Epi::PITCH);
 }
 
+// Sides of at most 128 (P = 64 or 128): B = a + b A + c A A and X^T <- X^T B in one launch.  A workgroup makes the 64
+// rows of B that its 64 x 64 tile of X^T needs from all of A in LDS (twice the tile's own work at P = 128, but nothing to wait
+// for), which saves the launch between the two products.  Small batches are bound by launches: 8 x 128 x 256 in fp32 takes
+// 80 us with three launches a step.
+template <int MODE, int P, bool SPLIT>
+__global__ __launch_bounds__(256) void narrow_kernel(const Args a, const uint8_t* A0, const uint8_t* A1, int64_t a_batch,
+                                                     float pa, float pb, float pc) {
+  constexpr int RB = 128, ST = P / 64;  // stages of 64 reduction values
+  constexpr int NA = SPLIT ? 2 : 1;
+  constexpr int A_ARR = P * RB, X_ARR = 64 * RB;             // one stage's rows, hi or lo
+  constexpr int A_ALL = ST * NA * A_ARR, X_ALL = ST * NA * X_ARR;
+  using Epi = Epilogue<MODE, 32, SPLIT>;
+  constexpr int EPI = 4 * 32 * Epi::PITCH * 4;
+  constexpr int FIRST = A_ALL > EPI ? A_ALL : EPI;           // A, then the epilogue's blocks
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[FIRST + 2 * X_ALL];
+  uint8_t *sa = smem, *sx = smem + FIRST, *sb = sx + X_ALL;  // [stage][hi, lo][row][RB]
+
+  const int lane = threadIdx.x & 63, wid = uniform_int(threadIdx.x >> 6), wm = wid >> 1, wn = wid & 1;
+  const int lr = lane & 31, lh = lane >> 5;
+  const TileAt at = tile_at<MODE>(a, tile::xcd_tile_index(gridDim.x, blockIdx.x));
+  const int e = at.e, m0 = at.mi * 64, n0 = at.ni * 64;
+  const int64_t row_bytes = (int64_t)P * 2;
+  const int row0 = m0 + wm * 32, col0 = n0 + wn * 32;
+  typename Epi::Elem el;
+  Epi::load(a, e, row0, col0, el);
+  // rows of 128 bytes, 8 per load instruction
+  auto load_rows = [&](const uint8_t* src, uint8_t* dst, int rows) {
+    const uint8_t* p = uniform_ptr(src);
+    for (int i = wid; i < rows / 8; i += 4) {
+      const int r = i * 8 + lane / 8;
+      load_lds16(p, (uint32_t)(r * row_bytes + (((lane % 8) ^ tile::swz<RB>(r)) << 4)), dst + i * 1024);
+    }
+  };
+#pragma unroll
+  for (int s = 0; s < ST; ++s) {
+    load_rows(A0 + e * a_batch + s * RB, sa + s * NA * A_ARR, P);
+    load_rows(a.M0 + e * a.m_batch + m0 * row_bytes + s * RB, sx + s * NA * X_ARR, 64);
+    if constexpr (SPLIT) {
+      load_rows(A1 + e * a_batch + s * RB, sa + (s * NA + 1) * A_ARR, P);
+      load_rows(a.M1 + e * a.m_batch + m0 * row_bytes + s * RB, sx + (s * NA + 1) * X_ARR, 64);
+    }
+  }
+  wait_vmcnt0();
+  __syncthreads();
+
+  // B^T: rows k (all P, half to each wm), columns the tile's 64 rows of B (32 to each wn)
+  constexpr int MB = ST;
+  f32x16_t acc[MB][1];
+  int krow[MB], irow[1] = {n0 + wn * 32 + lr};
+#pragma unroll
+  for (int i = 0; i < MB; ++i) {
+    krow[i] = wm * (P / 2) + i * 32 + lr;
+#pragma unroll
+    for (int v = 0; v < 16; ++v) acc[i][0][v] = 0.0f;
+  }
+  const tile::FragOff ko = tile::frag_offsets<RB, RB / 32>(krow[0], lh, 2);
+  const tile::FragOff io = tile::frag_offsets<RB, RB / 32>(irow[0], lh, 2);
+#pragma unroll
+  for (int s = 0; s < ST; ++s) {
+    const uint8_t* p = sa + s * NA * A_ARR;
+    if constexpr (SPLIT)
+      mma_stage_split<RB, MB, 1>(p, p, A_ARR, krow, irow, ko, io, acc);
+    else
+      tile::mma_stage_bf16<RB, MB, 1, f16x8_t>(p, p, krow, irow, ko, io, acc);
+  }
+  // accumulator values 4 q .. 4 q + 3 of a lane: B[i][k .. k + 3], i = irow, 8 bytes of row i
+#pragma unroll
+  for (int i = 0; i < MB; ++i)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int k = wm * (P / 2) + i * 32 + q * 8 + 4 * lh, r = irow[0], rb = wn * 32 + lr;
+      const int st = k / 64, ch = k % 64 / 8;
+      typedef _Float16 f16x4_t __attribute__((ext_vector_type(4)));
+      const f16x4_t ah = *reinterpret_cast<const f16x4_t*>(sa + st * NA * A_ARR + r * RB +
+                                                           ((ch ^ tile::swz<RB>(r)) << 4) + 8 * lh);
+      f16x4_t al = {0, 0, 0, 0}, bh, bl;
+      if constexpr (SPLIT)
+        al = *reinterpret_cast<const f16x4_t*>(sa + (st * NA + 1) * A_ARR + r * RB + ((ch ^ tile::swz<RB>(r)) << 4) +
+                                               8 * lh);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        float v = __builtin_fmaf(pb, (float)ah[x] + (float)al[x], pc * acc[i][0][4 * q + x]);
+        v += k + x == r ? pa : 0.0f;
+        _Float16 hi, lo;
+        split16(v, hi, lo);
+        bh[x] = hi;
+        bl[x] = lo;
+      }
+      uint8_t* d = sb + st * NA * X_ARR + rb * RB + ((ch ^ tile::swz<RB>(rb)) << 4) + 8 * lh;
+      *reinterpret_cast<f16x4_t*>(d) = bh;
+      if constexpr (SPLIT) *reinterpret_cast<f16x4_t*>(d + X_ARR) = bl;
+    }
+  __syncthreads();  // B is whole, and A is read no more
+
+  f32x16_t out[1][1];
+  int jrow[1] = {wm * 32 + lr}, brow[1] = {wn * 32 + lr};
+#pragma unroll
+  for (int v = 0; v < 16; ++v) out[0][0][v] = 0.0f;
+  const tile::FragOff jo = tile::frag_offsets<RB, RB / 32>(jrow[0], lh, 2);
+  const tile::FragOff bo = tile::frag_offsets<RB, RB / 32>(brow[0], lh, 2);
+#pragma unroll
+  for (int s = 0; s < ST; ++s) {
+    const uint8_t *px = sx + s * NA * X_ARR, *pb2 = sb + s * NA * X_ARR;
+    if constexpr (SPLIT)
+      mma_stage_split<RB, 1, 1>(px, pb2, X_ARR, jrow, brow, jo, bo, out);
+    else
+      tile::mma_stage_bf16<RB, 1, 1, f16x8_t>(px, pb2, jrow, brow, jo, bo, out);
+  }
+  Epi::run(a, e, row0, col0, false, out[0], el, reinterpret_cast<float*>(sa) + wid * 32 * Epi::PITCH);
+}
+
 // Four consecutive values of g from index i on, at the elements' own alignment (one wide access), zeros from `end` on
 typedef float f32x4_e4_t __attribute__((ext_vector_type(4), aligned(4)));
 typedef uint16_t u16x4_e2_t __attribute__((ext_vector_type(4), aligned(2)));
@@ -697,6 +812,7 @@ constexpr int CUS = 256, MOST_PARTS = 8;
 // parts of each of the others.
 struct Shape {
   int size, whole, parts, rest;
+  double us;  // estimate
 };
 
 // Microseconds of a product, to choose by: a launch of its own, then for every 256 tiles (one per compute unit; two smaller
@@ -710,7 +826,7 @@ constexpr double LAUNCH_US = 4.5, BYTES_PER_US = 4e6;
 
 static Shape shape(int64_t batch, int rows, int cols, int K, bool sym, int most_size, bool split) {
   Shape best{};
-  double best_us = 1e30;
+  best.us = 1e30;
   for (int size = 0; size <= most_size; ++size) {
     const int64_t nt = cols / TILE[size];
     const int64_t tiles = (sym ? nt * (nt + 1) / 2 : (int64_t)(rows / TILE[size]) * nt) * batch;
@@ -726,8 +842,8 @@ static Shape shape(int64_t batch, int rows, int cols, int K, bool sym, int most_
       const double bytes = 2.0 * rest * x * TILE[size] * TILE[size] * sizeof(float);
       const double us = LAUNCH_US + full * (red + epi) +
                         (rest == 0 ? 0.0 : x == 1 ? red + epi : red / x + LAUNCH_US + bytes / BYTES_PER_US);
-      if (us < best_us) {
-        best_us = us;
+      if (us < best.us) {
+        best.us = us;
         best.size = size;
         best.parts = x;
         best.rest = x > 1 ? rest : 0;
@@ -743,7 +859,8 @@ static size_t partial_bytes(const Shape& z) {
 
 struct Plan {
   int p, q, P, Q;
-  bool flip;
+  bool split, flip, narrow;
+  double us;  // of a step, estimated
   int chunks;
   int64_t chunk_values;
   Shape gram, poly, update;
@@ -753,20 +870,34 @@ struct Plan {
 
 static size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
 
-static Plan plan(int64_t batch, int m, int n, bool split) {
+static Plan plan_of(int64_t batch, int m, int n, bool split) {
   Plan z{};
+  z.split = split;
   z.flip = m > n;
   z.p = z.flip ? n : m;
   z.q = z.flip ? m : n;
-  // the largest tile that the products choose from sets the padding
-  auto tiles_of = [&](int t) { return (int64_t)((z.p + t - 1) / t) * ((z.q + t - 1) / t) * batch; };
-  const int most = tiles_of(256) >= CUS / 2 ? 2 : tiles_of(128) >= CUS / 2 ? 1 : 0;
-  const int tl = TILE[most];
-  z.P = (z.p + tl - 1) / tl * tl;
-  z.Q = (z.q + tl - 1) / tl * tl;
-  z.gram = shape(batch, z.P, z.P, z.Q, true, most, split);
-  z.poly = shape(batch, z.P, z.P, z.P, true, most, split);
-  z.update = shape(batch, z.Q, z.P, z.P, false, most, split);
+  // the largest tile that the products choose from sets the padding: the least sum of the estimates
+  z.us = 1e30;
+  for (int most = 0; most < 3; ++most) {
+    const int tl = TILE[most], P = (z.p + tl - 1) / tl * tl, Q = (z.q + tl - 1) / tl * tl;
+    const Shape gram = shape(batch, P, P, Q, true, most, split), poly = shape(batch, P, P, P, true, most, split),
+                update = shape(batch, Q, P, P, false, most, split);
+    if (gram.us + poly.us + update.us < z.us) {
+      z.us = gram.us + poly.us + update.us;
+      z.P = P;
+      z.Q = Q;
+      z.gram = gram;
+      z.poly = poly;
+      z.update = update;
+    }
+  }
+  // One launch for the last two products of a step: always at P = 64 (16 x 64 x 8192: 141 us against 162); at P = 128 while
+  // the rows of B that every tile makes for itself cost less than the launch: to four tiles per compute unit (16 x 128 x
+  // 2048: 120 us against 127; 64 x 128 x 1024: 157 against 148), with SPLIT to one (8 x 128 x 256: 64 us against 75;
+  // 2 x 128 x 8192: 156 against 152).
+  const int64_t narrow_tiles = (int64_t)(z.Q / 64) * (z.P / 64) * batch;
+  z.narrow = z.P == 64 || (z.P == 128 && narrow_tiles <= (split ? CUS : 4 * CUS));
+  if (z.narrow) z.us -= LAUNCH_US;
   const int64_t count = (int64_t)m * n;
   // chunks of 4096 values or more, 256 at most: a workgroup of the next kernel adds one per thread
   z.chunks = (int)(count / 4096 < 1 ? 1 : count / 4096 > 256 ? 256 : count / 4096);
@@ -776,9 +907,18 @@ static Plan plan(int64_t batch, int m, int n, bool split) {
   z.part_bytes = up256((size_t)batch * z.chunks * sizeof(double));
   for (const Shape* t : {&z.gram, &z.poly, &z.update})
     if (partial_bytes(*t) > z.partial) z.partial = partial_bytes(*t);
-  z.total = z.part_bytes + z.partial + (split ? 4 : 3) * z.x_bytes +
-            (split ? 4 : 2) * z.a_bytes;
+  z.total = z.part_bytes + z.partial + (split ? 4 : 3) * z.x_bytes + (split ? 4 : 2) * z.a_bytes;
   return z;
+}
+
+// bf16 results take the split form where the estimates are close: it brings them to their own rounding (1.7e-3 of the norm
+// off; a side of 64 and less is 2.5 to 2.9e-3 off without it, of 2048 2.0e-3), and a 64 x 64 takes 67 us either way, where
+// 4 x 100 x 1000 takes 91 us instead of 71.
+static Plan plan(int64_t batch, int m, int n, bool out_bf16) {
+  const Plan split = plan_of(batch, m, n, true);
+  if (!out_bf16) return split;
+  const Plan whole = plan_of(batch, m, n, false);
+  return split.us <= 1.2 * whole.us ? split : whole;
 }
 
 template <int MODE, int SIZE, bool SPLIT>
@@ -807,9 +947,22 @@ static void launch_product(const Args& a0, const Shape& z, int rows, int cols, h
     launch_sized<MODE, 0, SPLIT>(a, z, s);
 }
 
+template <int MODE, bool SPLIT>
+static void launch_narrow(const Args& a0, int Q, int P, int64_t batch, const uint8_t* A0, const uint8_t* A1, float pa,
+                          float pb, float pc, hipStream_t s) {
+  Args a = a0;
+  a.mt = Q / 64;
+  a.nt = P / 64;
+  const dim3 grid((unsigned)(a.mt * a.nt * batch));
+  const int64_t ab = (int64_t)P * P * 2;
+  if (P == 128)
+    hipLaunchKernelGGL((narrow_kernel<MODE, 128, SPLIT>), grid, dim3(256), 0, s, a, A0, A1, ab, pa, pb, pc);
+  else
+    hipLaunchKernelGGL((narrow_kernel<MODE, 64, SPLIT>), grid, dim3(256), 0, s, a, A0, A1, ab, pa, pb, pc);
+}
+
 template <bool SPLIT>
-static void run(const OrthLaunch& p, hipStream_t s) {
-  const Plan z = plan(p.batch, p.m, p.n, SPLIT);
+static void run(const OrthLaunch& p, const Plan& z, hipStream_t s) {
   uint8_t* ws = reinterpret_cast<uint8_t*>(p.workspace);
   auto take = [&](size_t bytes) {
     uint8_t* r = ws;
@@ -871,7 +1024,7 @@ static void run(const OrthLaunch& p, hipStream_t s) {
     q.alpha = p.b;
     q.beta = p.c / S;
     q.diag = p.a * S;
-    launch_product<POLY, SPLIT>(q, z.poly, z.P, z.P, s);
+    if (!z.narrow) launch_product<POLY, SPLIT>(q, z.poly, z.P, z.P, s);
     q.M0 = y0[cur];  // X^T <- X^T B
     q.M1 = y1[cur];
     q.m_batch = xb;
@@ -879,12 +1032,15 @@ static void run(const OrthLaunch& p, hipStream_t s) {
     q.N1 = b1;
     q.E1 = y1[cur];
     q.R0 = y0[nxt];
-    q.R1 = y1[nxt];
+    q.R1 = SPLIT || k + 2 < p.steps ? y1[nxt] : nullptr;  // the last step's X is hi alone without SPLIT
     q.r_batch = xb;
     if (k + 1 < p.steps) {
       q.alpha = p.a;
       q.beta = 1.0f / S;
-      launch_product<UPDATE, SPLIT>(q, z.update, z.Q, z.P, s);
+      if (z.narrow)
+        launch_narrow<UPDATE, SPLIT>(q, z.Q, z.P, p.batch, a0, a1, p.a * S, p.b, p.c / S, s);
+      else
+        launch_product<UPDATE, SPLIT>(q, z.update, z.Q, z.P, s);
     } else {
       q.alpha = p.a * (p.scale / S);
       q.beta = p.scale / S / S;
@@ -894,7 +1050,10 @@ static void run(const OrthLaunch& p, hipStream_t s) {
       q.turn = !z.flip;
       q.out_bf16 = p.out_bf16;
       q.out_vec = p.n % 8 == 0 && (uintptr_t)p.out % 16 == 0;
-      launch_product<FINAL, SPLIT>(q, z.update, z.Q, z.P, s);
+      if (z.narrow)
+        launch_narrow<FINAL, SPLIT>(q, z.Q, z.P, p.batch, a0, a1, p.a * S, p.b, p.c / S, s);
+      else
+        launch_product<FINAL, SPLIT>(q, z.update, z.Q, z.P, s);
     }
   }
 }
@@ -902,14 +1061,15 @@ static void run(const OrthLaunch& p, hipStream_t s) {
 }  // namespace orth
 
 size_t orthogonalize_workspace(int64_t batch, int m, int n, bool out_bf16) {
-  return orth::plan(batch, m, n, !out_bf16).total;
+  return orth::plan(batch, m, n, out_bf16).total;
 }
 
 void launch_orthogonalize(const OrthLaunch& p, hipStream_t s) {
-  if (p.out_bf16)
-    orth::run<false>(p, s);
+  const orth::Plan z = orth::plan(p.batch, p.m, p.n, p.out_bf16);
+  if (z.split)
+    orth::run<true>(p, z, s);
   else
-    orth::run<true>(p, s);
+    orth::run<false>(p, z, s);
 }
 
 }  // namespace moe

@@ -70,9 +70,12 @@ def test_sizes(B, mm, n, g_dtype, out_dtype):
 
 
 @pytest.mark.parametrize("B,mm,n,out_dtype", [(4, 2048, 2048, torch.bfloat16), (70, 512, 520, torch.bfloat16),
-                                              (40, 384, 1000, torch.float32), (26, 1300, 520, torch.bfloat16)])
+                                              (40, 384, 1000, torch.float32), (26, 1300, 520, torch.bfloat16),
+                                              (70, 128, 1000, torch.bfloat16), (70, 1000, 100, torch.float32),
+                                              (90, 60, 2000, torch.float32), (33, 192, 1100, torch.bfloat16),
+                                              (1, 1700, 5000, torch.bfloat16), (1, 5000, 1100, torch.float32)])
 def test_large_tiles(B, mm, n, out_dtype):
-    """Batches that fill the GPU with 256 x 256 tiles, partial tiles among them."""
+    """Every tile size, whole and shared tiles, the one-launch form of narrow matrices and the sizes past it."""
     g = normal(1, B, mm, n) * 1e-3
     out = m.moe_orthogonalize(g, out_dtype=out_dtype)
     check(out, definition(g))
