@@ -34,6 +34,10 @@ namespace orth {
 
 constexpr float S = 4096.0f;
 
+// 16 bytes at the elements' own alignment: one wide access
+typedef float f32x4_e4_t __attribute__((ext_vector_type(4), aligned(4)));
+typedef int i32x4_e2_t __attribute__((ext_vector_type(4), aligned(2)));
+
 enum Mode { GRAM = 0, POLY = 1, UPDATE = 2, FINAL = 3 };
 
 // Tiles.  0: 64 x 64 over 4 wavefronts (32 x 32 each); 1: 128 x 128 over 4 (64 x 64 each); 2: 256 x 256 over 8
@@ -87,7 +91,7 @@ struct Args {
   // FINAL: out [m][n]; turn: row i of the result is column i of out
   uint8_t* out;
   int m, n;
-  bool turn, out_bf16, out_vec;
+  bool turn, out_bf16;
 };
 
 // fp16 pair of a value: hi = rounded, lo = the rest rounded
@@ -274,29 +278,31 @@ struct Epilogue {
     }
   }
 
+  // 8 values of a row of out from column gc on, at the elements' own alignment; a row's last ones go one by one
   static MOE_DEV void store_out(const Args& a, int64_t o, int gc, const float (&v)[8]) {
+    if (gc + 8 <= a.n) {
+      if (a.out_bf16) {
+        i32x4_t w;
 #pragma unroll
-    for (int x = 0; x < 8; ++x)
+        for (int d = 0; d < 4; ++d)
+          w[d] = (int)((uint32_t)f32_to_bf16_bits(v[2 * d]) | ((uint32_t)f32_to_bf16_bits(v[2 * d + 1]) << 16));
+        *reinterpret_cast<i32x4_e2_t*>(a.out + o * 2) = w;
+      } else {
+#pragma unroll
+        for (int d = 0; d < 2; ++d)
+          *reinterpret_cast<f32x4_e4_t*>(a.out + o * 4 + 16 * d) =
+              (f32x4_t){v[4 * d], v[4 * d + 1], v[4 * d + 2], v[4 * d + 3]};
+      }
+      return;
+    }
+#pragma unroll
+    for (int x = 0; x < 7; ++x)
       if (gc + x < a.n) {
         if (a.out_bf16)
           reinterpret_cast<uint16_t*>(a.out)[o + x] = f32_to_bf16_bits(v[x]);
         else
           reinterpret_cast<float*>(a.out)[o + x] = v[x];
       }
-  }
-  static MOE_DEV void store_out8(const Args& a, int64_t o, const float (&v)[8]) {
-    if (a.out_bf16) {
-      i32x4_t w;
-#pragma unroll
-      for (int d = 0; d < 4; ++d)
-        w[d] = (int)((uint32_t)f32_to_bf16_bits(v[2 * d]) | ((uint32_t)f32_to_bf16_bits(v[2 * d + 1]) << 16));
-      *reinterpret_cast<i32x4_t*>(a.out + o * 2) = w;
-    } else {
-#pragma unroll
-      for (int d = 0; d < 2; ++d)
-        *reinterpret_cast<f32x4_t*>(a.out + o * 4 + 16 * d) =
-            (f32x4_t){v[4 * d], v[4 * d + 1], v[4 * d + 2], v[4 * d + 3]};
-    }
   }
   static MOE_DEV void store_pair(const Args& a, int64_t at, const float (&v)[8]) {
     f16x8_t h, l;
@@ -349,13 +355,7 @@ struct Epilogue {
       }
       if constexpr (MODE == FINAL) {
         const int gr = row0 + r, gc = col0 + c;
-        if (!turn && gr < a.m && gc < a.n) {
-          const int64_t o = ((int64_t)e * a.m + gr) * a.n + gc;
-          if (a.out_vec)  // n a multiple of 8: the 8 values are all inside, and aligned
-            store_out8(a, o, v);
-          else
-            store_out(a, o, gc, v);
-        }
+        if (!turn && gr < a.m && gc < a.n) store_out(a, ((int64_t)e * a.m + gr) * a.n + gc, gc, v);
       } else {
         store_pair(a, e * a.r_batch + ((int64_t)(row0 + r) * a.ld + col0 + c) * 2, v);
       }
@@ -375,13 +375,7 @@ struct Epilogue {
       for (int x = 0; x < 8; ++x) v[x] = sc[(r + x) * PITCH + c];
       const int gr = col0 + c, gc = row0 + r;  // row and first column of what is stored
       if constexpr (MODE == FINAL) {
-        if (gr < a.m && gc < a.n) {
-          const int64_t o = ((int64_t)e * a.m + gr) * a.n + gc;
-          if (a.out_vec)
-            store_out8(a, o, v);
-          else
-            store_out(a, o, gc, v);
-        }
+        if (gr < a.m && gc < a.n) store_out(a, ((int64_t)e * a.m + gr) * a.n + gc, gc, v);
       } else {
         store_pair(a, e * a.r_batch + ((int64_t)gr * a.ld + gc) * 2, v);
       }
@@ -685,7 +679,6 @@ __global__ __launch_bounds__(256) void narrow_kernel(const Args a, const uint8_t
 }
 
 // Four consecutive values of g from index i on, at the elements' own alignment (one wide access), zeros from `end` on
-typedef float f32x4_e4_t __attribute__((ext_vector_type(4), aligned(4)));
 typedef uint16_t u16x4_e2_t __attribute__((ext_vector_type(4), aligned(2)));
 MOE_DEV f32x4_t load_g4(const uint8_t* g, bool bf16, int64_t i, int64_t end) {
   f32x4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -1049,7 +1042,6 @@ static void run(const OrthLaunch& p, const Plan& z, hipStream_t s) {
       q.n = p.n;
       q.turn = !z.flip;
       q.out_bf16 = p.out_bf16;
-      q.out_vec = p.n % 8 == 0 && (uintptr_t)p.out % 16 == 0;
       if (z.narrow)
         launch_narrow<FINAL, SPLIT>(q, z.Q, z.P, p.batch, a0, a1, p.a * S, p.b, p.c / S, s);
       else

@@ -97,7 +97,8 @@ def test_orthogonalize_refuses(bad, says):
 def test_orthogonalize_workspace_and_types():
     need = m.moe_orthogonalize_workspace_bytes(2, 64, 96)
     assert need > 0
-    assert m.moe_orthogonalize_workspace_bytes(2, 64, 96, torch.float32) > need
+    assert (m.moe_orthogonalize_workspace_bytes(4, 2048, 4096, torch.float32)
+            > m.moe_orthogonalize_workspace_bytes(4, 2048, 4096))
     assert m.moe_orthogonalize_workspace_bytes(2, 96, 64) == need
     assert orth(wsb=need - 1) == m.MOE_ERR_WORKSPACE
     assert orth(ws=None) == m.MOE_ERR_WORKSPACE
