@@ -25,6 +25,8 @@
 // B [P][P]; P and Q are p and q rounded up to the tile size and zero-filled, which the iteration keeps, so no product has
 // a bound to check.  Every product is C[i][j] = sum_k M[i][k] N[j][k] with both reductions contiguous: X X^T from X
 // twice, A A from A twice (symmetric), B X from B and the transpose of X.
+#include <utility>
+
 #include "common.h"
 #include "gemm_tile.h"
 #include "kernels.h"
@@ -88,10 +90,10 @@ struct Args {
   // the first `whole` tiles are one workgroup each; `parts` workgroups share each of the rest
   int whole, parts;
   float* partial;            // [rest * parts][tile values]
-  // FINAL: out [m][n]; turn: row i of the result is column i of out
+  // FINAL: out [m][n], the result's rows and columns
   uint8_t* out;
   int m, n;
-  bool turn, out_bf16;
+  bool out_bf16;
 };
 
 // fp16 pair of a value: hi = rounded, lo = the rest rounded
@@ -254,7 +256,7 @@ MOE_DEV TileAt tile_at(const Args& a, int L) {
 
 // What follows a product for one 32 x W block of a wavefront (W = WTN columns), through the wavefront's own LDS block, so
 // that every global access is 16 bytes per lane: by rows for the result (and the elementwise operand, loaded ahead by the
-// caller), by columns for a transposed one.
+// caller), by columns for a mirrored one.
 // Accumulator element v of a lane: row (v / 4) * 8 + 4 * (lane / 32) + v % 4, column lane % 32.
 template <int MODE, int W, bool SPLIT>
 struct Epilogue {
@@ -329,7 +331,6 @@ struct Epilogue {
 #pragma unroll
       for (int v = 0; v < 16; ++v) sc[((v >> 2) * 8 + 4 * lh + (v & 3)) * PITCH + j * 32 + lr] = acc[j][v];
     wave_lds_fence();
-    const bool turn = MODE == FINAL ? a.turn : SYM && mirror;
 #pragma unroll
     for (int it = 0; it < PASS; ++it) {
       const int r = it * RPP + lane / LPR, c = lane % LPR * 8;
@@ -355,30 +356,25 @@ struct Epilogue {
       }
       if constexpr (MODE == FINAL) {
         const int gr = row0 + r, gc = col0 + c;
-        if (!turn && gr < a.m && gc < a.n) store_out(a, ((int64_t)e * a.m + gr) * a.n + gc, gc, v);
+        if (gr < a.m && gc < a.n) store_out(a, ((int64_t)e * a.m + gr) * a.n + gc, gc, v);
       } else {
         store_pair(a, e * a.r_batch + ((int64_t)(row0 + r) * a.ld + col0 + c) * 2, v);
       }
-      if (turn)
+      if (SYM && mirror)
 #pragma unroll
         for (int d = 0; d < 2; ++d)
           *reinterpret_cast<f32x4_t*>(&sc[r * PITCH + c + 4 * d]) =
               (f32x4_t){v[4 * d], v[4 * d + 1], v[4 * d + 2], v[4 * d + 3]};
     }
     wave_lds_fence();
-    if (!turn) return;
+    if (!SYM || !mirror) return;
 #pragma unroll
     for (int it = 0; it < W / 16; ++it) {
       const int c = it * 16 + lane / 4, r = lane % 4 * 8;
       float v[8];
 #pragma unroll
       for (int x = 0; x < 8; ++x) v[x] = sc[(r + x) * PITCH + c];
-      const int gr = col0 + c, gc = row0 + r;  // row and first column of what is stored
-      if constexpr (MODE == FINAL) {
-        if (gr < a.m && gc < a.n) store_out(a, ((int64_t)e * a.m + gr) * a.n + gc, gc, v);
-      } else {
-        store_pair(a, e * a.r_batch + ((int64_t)gr * a.ld + gc) * 2, v);
-      }
+      store_pair(a, e * a.r_batch + ((int64_t)(col0 + c) * a.ld + row0 + r) * 2, v);
     }
     wave_lds_fence();
   }
@@ -573,7 +569,7 @@ __global__ __launch_bounds__(256) void join_kernel(const Args a) {
 // 80 us with three launches a step.
 template <int MODE, int P, bool SPLIT>
 __global__ __launch_bounds__(256) void narrow_kernel(const Args a, const uint8_t* A0, const uint8_t* A1, int64_t a_batch,
-                                                     float pa, float pb, float pc) {
+                                                     bool b_first, float pa, float pb, float pc) {
   constexpr int RB = 128, ST = P / 64;  // stages of 64 reduction values
   constexpr int NA = SPLIT ? 2 : 1;
   constexpr int A_ARR = P * RB, X_ARR = 64 * RB;             // one stage's rows, hi or lo
@@ -587,9 +583,9 @@ __global__ __launch_bounds__(256) void narrow_kernel(const Args a, const uint8_t
   const int lane = threadIdx.x & 63, wid = uniform_int(threadIdx.x >> 6), wm = wid >> 1, wn = wid & 1;
   const int lr = lane & 31, lh = lane >> 5;
   const TileAt at = tile_at<MODE>(a, tile::xcd_tile_index(gridDim.x, blockIdx.x));
-  const int e = at.e, m0 = at.mi * 64, n0 = at.ni * 64;
+  const int e = at.e, row0 = at.mi * 64 + wm * 32, col0 = at.ni * 64 + wn * 32;  // of the result
+  const int m0 = (b_first ? at.ni : at.mi) * 64, n0 = (b_first ? at.mi : at.ni) * 64;  // rows of X^T and of B
   const int64_t row_bytes = (int64_t)P * 2;
-  const int row0 = m0 + wm * 32, col0 = n0 + wn * 32;
   typename Epi::Elem el;
   Epi::load(a, e, row0, col0, el);
   // rows of 128 bytes, 8 per load instruction
@@ -669,11 +665,11 @@ __global__ __launch_bounds__(256) void narrow_kernel(const Args a, const uint8_t
   const tile::FragOff bo = tile::frag_offsets<RB, RB / 32>(brow[0], lh, 2);
 #pragma unroll
   for (int s = 0; s < ST; ++s) {
-    const uint8_t *px = sx + s * NA * X_ARR, *pb2 = sb + s * NA * X_ARR;
+    const uint8_t *pm = (b_first ? sb : sx) + s * NA * X_ARR, *pn = (b_first ? sx : sb) + s * NA * X_ARR;
     if constexpr (SPLIT)
-      mma_stage_split<RB, 1, 1>(px, pb2, X_ARR, jrow, brow, jo, bo, out);
+      mma_stage_split<RB, 1, 1>(pm, pn, X_ARR, jrow, brow, jo, bo, out);
     else
-      tile::mma_stage_bf16<RB, 1, 1, f16x8_t>(px, pb2, jrow, brow, jo, bo, out);
+      tile::mma_stage_bf16<RB, 1, 1, f16x8_t>(pm, pn, jrow, brow, jo, bo, out);
   }
   Epi::run(a, e, row0, col0, false, out[0], el, reinterpret_cast<float*>(sa) + wid * 32 * Epi::PITCH);
 }
@@ -941,17 +937,22 @@ static void launch_product(const Args& a0, const Shape& z, int rows, int cols, h
 }
 
 template <int MODE, bool SPLIT>
-static void launch_narrow(const Args& a0, int Q, int P, int64_t batch, const uint8_t* A0, const uint8_t* A1, float pa,
-                          float pb, float pc, hipStream_t s) {
+static void launch_narrow(const Args& a0, int rows, int cols, bool b_first, int P, int64_t batch, const uint8_t* A0,
+                          const uint8_t* A1, float pa, float pb, float pc, hipStream_t s) {
   Args a = a0;
-  a.mt = Q / 64;
-  a.nt = P / 64;
+  a.mt = rows / 64;
+  a.nt = cols / 64;
+  if (b_first) {  // the kernel takes X^T as M and its tiles' rows of B from A
+    a.M0 = a0.N0;
+    a.M1 = a0.N1;
+    a.m_batch = a0.n_batch;
+  }
   const dim3 grid((unsigned)(a.mt * a.nt * batch));
   const int64_t ab = (int64_t)P * P * 2;
   if (P == 128)
-    hipLaunchKernelGGL((narrow_kernel<MODE, 128, SPLIT>), grid, dim3(256), 0, s, a, A0, A1, ab, pa, pb, pc);
+    hipLaunchKernelGGL((narrow_kernel<MODE, 128, SPLIT>), grid, dim3(256), 0, s, a, A0, A1, ab, b_first, pa, pb, pc);
   else
-    hipLaunchKernelGGL((narrow_kernel<MODE, 64, SPLIT>), grid, dim3(256), 0, s, a, A0, A1, ab, pa, pb, pc);
+    hipLaunchKernelGGL((narrow_kernel<MODE, 64, SPLIT>), grid, dim3(256), 0, s, a, A0, A1, ab, b_first, pa, pb, pc);
 }
 
 template <bool SPLIT>
@@ -1031,7 +1032,7 @@ static void run(const OrthLaunch& p, const Plan& z, hipStream_t s) {
       q.alpha = p.a;
       q.beta = 1.0f / S;
       if (z.narrow)
-        launch_narrow<UPDATE, SPLIT>(q, z.Q, z.P, p.batch, a0, a1, p.a * S, p.b, p.c / S, s);
+        launch_narrow<UPDATE, SPLIT>(q, z.Q, z.P, false, z.P, p.batch, a0, a1, p.a * S, p.b, p.c / S, s);
       else
         launch_product<UPDATE, SPLIT>(q, z.update, z.Q, z.P, s);
     } else {
@@ -1040,12 +1041,17 @@ static void run(const OrthLaunch& p, const Plan& z, hipStream_t s) {
       q.out = reinterpret_cast<uint8_t*>(p.out);
       q.m = p.m;
       q.n = p.n;
-      q.turn = !z.flip;
       q.out_bf16 = p.out_bf16;
+      if (!z.flip) {  // the last product as B X: its rows are then out's
+        std::swap(q.M0, q.N0);
+        std::swap(q.M1, q.N1);
+        std::swap(q.m_batch, q.n_batch);
+      }
+      const int rows = z.flip ? z.Q : z.P, cols = z.flip ? z.P : z.Q;
       if (z.narrow)
-        launch_narrow<FINAL, SPLIT>(q, z.Q, z.P, p.batch, a0, a1, p.a * S, p.b, p.c / S, s);
+        launch_narrow<FINAL, SPLIT>(q, rows, cols, !z.flip, z.P, p.batch, a0, a1, p.a * S, p.b, p.c / S, s);
       else
-        launch_product<FINAL, SPLIT>(q, z.update, z.Q, z.P, s);
+        launch_product<FINAL, SPLIT>(q, z.update, rows, cols, s);
     }
   }
 }
