@@ -457,16 +457,14 @@ def moe_combine_slots(y_slot, topk_idx, e_lo=0, E_local=None, out_dtype=torch.bf
     return out
 
 
-_CURRENT = contextlib.nullcontext()
-
-
-def _on_device(fn, dev, stream):
-    """Context of a call on tensors of device ``dev``: kernels are launched with that device current."""
-    if dev.type != "cuda":
-        raise ValueError(f"{fn}: tensors must be on the GPU (got {dev})")
-    if stream is not None and isinstance(stream, torch.cuda.Stream) and stream.device != dev:
-        raise ValueError(f"{fn}: the stream is on {stream.device}, the tensors on {dev}")
-    return _CURRENT if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+def _elsewhere(fn, index, stream) -> bool:
+    """Whether the tensors' GPU ``index`` is not the current device: the call is then made again with it current, since
+    kernels are launched there.  Tensors on the CPU (-1) and streams of another device are refused."""
+    if index < 0:
+        raise ValueError(f"{fn}: tensors must be on the GPU")
+    if stream is not None and isinstance(stream, torch.cuda.Stream) and stream.device.index != index:
+        raise ValueError(f"{fn}: the stream is on {stream.device}, the tensors on cuda:{index}")
+    return torch._C._cuda_getDevice() != index
 
 
 def _tensor(fn, name, t, shape, dtypes, index):
@@ -537,7 +535,7 @@ def moe_norm(x, weight, bias=None, residual=None, kind="layer", eps=1e-5, out_dt
     out_dtype: x's (default), or torch.float8_e4m3fn / torch.uint8: e4m3 codes with y_scales [T, H/128], as
     moe_dispatch_permute takes them.  ``sum`` may be x or residual themselves."""
     fn = "moe_norm"
-    shape, dt, index, kind, w_ptr = _norm_args(fn, x, weight, kind)
+    shape, dt, index, code, w_ptr = _norm_args(fn, x, weight, kind)
     T, H = shape
     x_ptr, ldx = _rows(fn, "x", x, shape, dt, index)
     r_ptr, ldr = (None, 0) if residual is None else _rows(fn, "residual", residual, shape, dt, index)
@@ -550,29 +548,31 @@ def moe_norm(x, weight, bias=None, residual=None, kind="layer", eps=1e-5, out_dt
         raise NotImplementedError(f"{fn}: the output is the rows' dtype or e4m3 codes, not {yt}")
     if fp8 and H % 128:
         raise ValueError(f"{fn}: e4m3 rows need H = {H} to be a multiple of 128")
-    layer = kind == MOE_NORM_LAYER
-    with _on_device(fn, x.device, stream):
-        if (y is None or rstd is None or (fp8 and y_scales is None) or (layer and mean is None)
-                or (residual is not None and sum is None)):
-            dev = x.device
-            with _alloc_on(stream):
-                if y is None:
-                    y = torch.empty((T, H), dtype=yt, device=dev)
-                if fp8 and y_scales is None:
-                    y_scales = torch.empty((T, H // 128), dtype=torch.float32, device=dev)
-                if residual is not None and sum is None:
-                    sum = torch.empty((T, H), dtype=dt, device=dev)
-                if layer and mean is None:
-                    mean = torch.empty(T, dtype=torch.float32, device=dev)
-                if rstd is None:
-                    rstd = torch.empty(T, dtype=torch.float32, device=dev)
-        y_ptr = _tensor(fn, "y", y, shape, (yt,), index)
-        rstd_ptr = _tensor(fn, "rstd", rstd, shape[:1], _F32, index)
-        ys_ptr = _tensor(fn, "y_scales", y_scales, (T, H // 128), _F32, index) if fp8 else None
-        mean_ptr = _tensor(fn, "mean", mean, shape[:1], _F32, index) if layer else None
-        sum_ptr = None if residual is None else _tensor(fn, "sum", sum, shape, (dt,), index)
-        st = lib.moe_norm(x_ptr, ldx, r_ptr, ldr, _CODES[dt], T, H, kind, w_ptr, b_ptr, _CODES[weight.dtype], eps,
-                          sum_ptr, y_ptr, ys_ptr, _CODES[yt], mean_ptr, rstd_ptr, _stream(stream, index))
+    layer = code == MOE_NORM_LAYER
+    if _elsewhere(fn, index, stream):
+        with torch.cuda.device(index):
+            return moe_norm(x, weight, bias, residual, kind, eps, out_dtype, y, y_scales, sum, mean, rstd, stream)
+    if (y is None or rstd is None or (fp8 and y_scales is None) or (layer and mean is None)
+            or (residual is not None and sum is None)):
+        dev = x.device
+        with _alloc_on(stream):
+            if y is None:
+                y = torch.empty((T, H), dtype=yt, device=dev)
+            if fp8 and y_scales is None:
+                y_scales = torch.empty((T, H // 128), dtype=torch.float32, device=dev)
+            if residual is not None and sum is None:
+                sum = torch.empty((T, H), dtype=dt, device=dev)
+            if layer and mean is None:
+                mean = torch.empty(T, dtype=torch.float32, device=dev)
+            if rstd is None:
+                rstd = torch.empty(T, dtype=torch.float32, device=dev)
+    y_ptr = _tensor(fn, "y", y, shape, (yt,), index)
+    rstd_ptr = _tensor(fn, "rstd", rstd, shape[:1], _F32, index)
+    ys_ptr = _tensor(fn, "y_scales", y_scales, (T, H // 128), _F32, index) if fp8 else None
+    mean_ptr = _tensor(fn, "mean", mean, shape[:1], _F32, index) if layer else None
+    sum_ptr = None if residual is None else _tensor(fn, "sum", sum, shape, (dt,), index)
+    st = lib.moe_norm(x_ptr, ldx, r_ptr, ldr, _CODES[dt], T, H, code, w_ptr, b_ptr, _CODES[weight.dtype], eps,
+                      sum_ptr, y_ptr, ys_ptr, _CODES[yt], mean_ptr, rstd_ptr, _stream(stream, index))
     if st:
         _check(st, fn)
     return Norm(y, y_scales if fp8 else None, x if residual is None else sum, mean if layer else None, rstd)
@@ -590,9 +590,9 @@ def moe_norm_backward(dy, rows, weight, mean, rstd, kind="layer", dsum=None, wan
     residual stream) added.  dx may be dy or dsum themselves (out["dx"]).  want_bias: default, for kind "layer" only
     (with ``out``: where out["dbias"] is given)."""
     fn = "moe_norm_backward"
-    shape, dt, index, kind, w_ptr = _norm_args(fn, rows, weight, kind)
+    shape, dt, index, code, w_ptr = _norm_args(fn, rows, weight, kind)
     T, H = shape
-    layer = kind == MOE_NORM_LAYER
+    layer = code == MOE_NORM_LAYER
     if want_bias is None:
         want_bias = layer if out is None else out.get("dbias") is not None
     s_ptr, ld_s = _rows(fn, "rows", rows, shape, dt, index)
@@ -602,25 +602,27 @@ def moe_norm_backward(dy, rows, weight, mean, rstd, kind="layer", dsum=None, wan
         raise ValueError(f"{fn}: kind 'layer' needs the rows' means")
     mean_ptr = _tensor(fn, "mean", mean, shape[:1], _F32, index) if layer else None
     rstd_ptr = _tensor(fn, "rstd", rstd, shape[:1], _F32, index)
-    with _on_device(fn, rows.device, stream):
-        if out is None or workspace is None:
-            dev = rows.device
-            with _alloc_on(stream):
-                if out is None:
-                    out = dict(dx=torch.empty((T, H), dtype=dt, device=dev),
-                               dweight=torch.empty(H, dtype=torch.float32, device=dev),
-                               dbias=torch.empty(H, dtype=torch.float32, device=dev) if want_bias else None)
-                if workspace is None:
-                    workspace = torch.empty(moe_norm_backward_workspace_bytes(T, H), dtype=torch.uint8, device=dev)
-        dx_ptr = _tensor(fn, "dx", out["dx"], shape, (dt,), index)
-        dw_ptr = _tensor(fn, "dweight", out["dweight"], shape[1:], _F32, index)
-        if want_bias and out.get("dbias") is None:
-            raise ValueError(f"{fn}: want_bias needs out['dbias']")
-        db_ptr = _tensor(fn, "dbias", out["dbias"], shape[1:], _F32, index) if want_bias else None
-        ws_ptr, ws_bytes = _workspace(fn, workspace, index)
-        st = lib.moe_norm_backward(dy_ptr, ld_dy, s_ptr, ld_s, ds_ptr, ld_ds, _CODES[dt], T, H, kind, w_ptr,
-                                   _CODES[weight.dtype], mean_ptr, rstd_ptr, dx_ptr, dw_ptr, db_ptr, ws_ptr, ws_bytes,
-                                   _stream(stream, index))
+    if _elsewhere(fn, index, stream):
+        with torch.cuda.device(index):
+            return moe_norm_backward(dy, rows, weight, mean, rstd, kind, dsum, want_bias, out, workspace, stream)
+    if out is None or workspace is None:
+        dev = rows.device
+        with _alloc_on(stream):
+            if out is None:
+                out = dict(dx=torch.empty((T, H), dtype=dt, device=dev),
+                           dweight=torch.empty(H, dtype=torch.float32, device=dev),
+                           dbias=torch.empty(H, dtype=torch.float32, device=dev) if want_bias else None)
+            if workspace is None:
+                workspace = torch.empty(moe_norm_backward_workspace_bytes(T, H), dtype=torch.uint8, device=dev)
+    dx_ptr = _tensor(fn, "dx", out["dx"], shape, (dt,), index)
+    dw_ptr = _tensor(fn, "dweight", out["dweight"], shape[1:], _F32, index)
+    if want_bias and out.get("dbias") is None:
+        raise ValueError(f"{fn}: want_bias needs out['dbias']")
+    db_ptr = _tensor(fn, "dbias", out["dbias"], shape[1:], _F32, index) if want_bias else None
+    ws_ptr, ws_bytes = _workspace(fn, workspace, index)
+    st = lib.moe_norm_backward(dy_ptr, ld_dy, s_ptr, ld_s, ds_ptr, ld_ds, _CODES[dt], T, H, code, w_ptr,
+                               _CODES[weight.dtype], mean_ptr, rstd_ptr, dx_ptr, dw_ptr, db_ptr, ws_ptr, ws_bytes,
+                               _stream(stream, index))
     if st:
         _check(st, fn)
     return out
@@ -661,19 +663,21 @@ def moe_orthogonalize(g, steps=5, coeffs=ORTHOGONALIZE_COEFFS, eps=1e-7, scale=1
     ot = out.dtype if out is not None else out_dtype or torch.bfloat16
     if ot not in _ROW_TYPES:
         raise ValueError(f"{fn}: the output must be float32 or bfloat16 (got {ot})")
-    with _on_device(fn, g.device, stream):
-        if out is None or workspace is None:
-            with _alloc_on(stream):
-                if out is None:
-                    out = torch.empty(g.shape, dtype=ot, device=g.device)
-                if workspace is None:
-                    workspace = torch.empty(moe_orthogonalize_workspace_bytes(B, m, n, ot), dtype=torch.uint8,
-                                            device=g.device)
-        out_ptr = _tensor(fn, "out", out, g.shape, (ot,), index)
-        if g_ptr < out_ptr + out.nbytes and out_ptr < g_ptr + g.nbytes:
-            raise ValueError(f"{fn}: out must not overlap g")
-        _check(lib.moe_orthogonalize(g_ptr, dtype_code(g.dtype), B, m, n, steps, *coeffs, eps, scale, out_ptr,
-                                     dtype_code(ot), *_workspace(fn, workspace, index), _stream(stream, index)), fn)
+    if _elsewhere(fn, index, stream):
+        with torch.cuda.device(index):
+            return moe_orthogonalize(g, steps, coeffs, eps, scale, out_dtype, out, workspace, stream)
+    if out is None or workspace is None:
+        with _alloc_on(stream):
+            if out is None:
+                out = torch.empty(g.shape, dtype=ot, device=g.device)
+            if workspace is None:
+                workspace = torch.empty(moe_orthogonalize_workspace_bytes(B, m, n, ot), dtype=torch.uint8,
+                                        device=g.device)
+    out_ptr = _tensor(fn, "out", out, g.shape, (ot,), index)
+    if g_ptr < out_ptr + out.nbytes and out_ptr < g_ptr + g.nbytes:
+        raise ValueError(f"{fn}: out must not overlap g")
+    _check(lib.moe_orthogonalize(g_ptr, dtype_code(g.dtype), B, m, n, steps, *coeffs, eps, scale, out_ptr,
+                                 dtype_code(ot), *_workspace(fn, workspace, index), _stream(stream, index)), fn)
     return out
 
 

@@ -1,6 +1,7 @@
 // C-ABI entry points of libmoe_ep: argument validation on the host (nothing is enqueued unless every
 // argument is valid), then kernel launches on the caller's stream.  No entry point synchronises, allocates or
 // reads device memory on the host.
+#include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
 
@@ -751,20 +752,25 @@ size_t moe_orthogonalize_workspace_bytes(int64_t batch, int32_t m, int32_t n, mo
   return orthogonalize_workspace(batch, m, n, out_dtype == MOE_DTYPE_BF16);
 }
 
-// Whether `steps` of s -> s (a + b s^2 + c s^4) from [0, 1] stay where the fp16 operands hold them: |s| <= 3, and
-// |a + b s^2 + c s^4| <= 12 (the operands carry a factor 2^12, and fp16 ends at 16 * 2^12).  The bounds are taken at 4097
-// points of each step's interval, with a factor 1.01 between steps for what lies between the points.
-static bool iteration_bounded(int32_t steps, float a, float b, float c) {
+// Whether `steps` of s -> s q(s^2), q(t) = a + b t + c t^2, from [0, 1] stay where the fp16 operands hold them: |s| <= 3 and
+// |q| <= 12 (the operands carry a factor 2^12, and fp16 ends at 16 * 2^12).  Both are extreme at the ends of the interval,
+// at q's vertex t = -b / (2 c) or where a + 3 b t + 5 c t^2 = 0; 1.01 between the steps is for what the operands' rounding
+// adds to a singular value.
+static bool iteration_bounded(int32_t steps, double a, double b, double c) {
   double hi = 1.0;
+  const double d = 9.0 * b * b - 20.0 * a * c, root = d > 0.0 ? sqrt(d) : 0.0;
   for (int32_t k = 0; k < steps; ++k) {
+    const double end = hi * hi;
+    const double at[5] = {0.0, end, c != 0.0 ? -b / (2.0 * c) : 0.0, c != 0.0 ? (-3.0 * b + root) / (10.0 * c) : 0.0,
+                          c != 0.0 ? (-3.0 * b - root) / (10.0 * c) : (b != 0.0 ? -a / (3.0 * b) : 0.0)};
     double next = 0.0;
-    for (int i = 0; i <= 4096; ++i) {
-      const double s = hi * i / 4096, s2 = s * s, q = (double)a + (double)b * s2 + (double)c * s2 * s2;
-      const double v = s * q;
+    for (double t : at) {
+      t = t > 0.0 ? (t < end ? t : end) : 0.0;  // outside: an end instead
+      const double q = a + b * t + c * t * t, v = sqrt(t) * q;
       if (!(q <= 12.0 && q >= -12.0 && v <= 3.0 && v >= -3.0)) return false;
       next = v > next ? v : (-v > next ? -v : next);
     }
-    hi = next * 1.01;
+    hi = 1.01 * next;
   }
   return true;
 }

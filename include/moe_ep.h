@@ -399,7 +399,8 @@ moe_status moe_norm(const void* x, int64_t ldx, const void* residual, int64_t ld
  *   mean, rstd  (device) [T] fp32 from moe_norm (mean unused for MOE_NORM_RMS).
  *   dx          (device) [T, H] in dtype out, contiguous; may be dy or dsum itself (contiguous rows).
  *   dweight, dbias (device) [H] fp32 out, written (not added to); dbias may be NULL.  T = 0 writes zeros.
- *   workspace   (device) at least moe_norm_backward_workspace_bytes(T, H) bytes, 256-byte aligned.
+ *   workspace   (device) at least moe_norm_backward_workspace_bytes(T, H) bytes, 256-byte aligned; calls that overlap
+ *               (other streams, graphs replayed at once) need one each.
  * Domain and alignment as moe_norm.
  */
 size_t moe_norm_backward_workspace_bytes(int64_t T, int32_t H);
@@ -417,11 +418,12 @@ moe_status moe_norm_backward(const void* dy, int64_t ld_dy, const void* s, int64
  *        with an infinity or a NaN gives NaN, and touches no other matrix of the batch.
  *   out  (device) [batch, m, n] out, out_dtype F32 or BF16; must not overlap g.
  * Precision: products of fp16 operands accumulated in fp32, X kept to 22 bits between the steps.  out_dtype BF16 takes
- * each operand to one fp16 value, scaled so that none is subnormal in earnest: |error|_F is about 1.5e-3 |out|_F, as
- * the rounding to bf16 itself.  F32 takes each operand to two (hi + lo, 22 bits) and three products: fp32's accuracy at
- * three times the products' cost.
+ * each operand to one fp16 value: with the rounding to bf16 |error|_F is 2.0 to 2.3e-3 |out|_F (the rounding alone is
+ * 1.7e-3; up to 2.8e-3 at rank 1).  F32 takes each operand to two (hi + lo, 22 bits) and three products: fp32's accuracy at
+ * three times the products' cost; so does BF16 where a batch is so small that this costs nothing.
  *   X's values are held to 2^-37 at least: a g whose norm is below about 1e-9 eps gives zeros.
- *   workspace (device) at least moe_orthogonalize_workspace_bytes(batch, m, n, out_dtype) bytes, 256-byte aligned.
+ *   workspace (device) at least moe_orthogonalize_workspace_bytes(batch, m, n, out_dtype) bytes, 256-byte aligned; calls
+ *        that overlap (other streams, graphs replayed at once) need one each.
  * Domain: batch >= 0, 1 <= m, n <= 65536, 1 <= steps <= 32, eps > 0 and finite, scale finite, and coefficients that keep
  * the iteration bounded: from singular values in [0, 1] every step's stay within 3, and those of a + b A + c A A within 12
  * (MOE_ERR_INVALID_ARG otherwise).  Results do not depend on run or launch order.
