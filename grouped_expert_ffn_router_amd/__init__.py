@@ -505,7 +505,7 @@ _CODES = {torch.float32: MOE_DTYPE_F32, torch.bfloat16: MOE_DTYPE_BF16, torch.ui
           torch.float8_e4m3fn: MOE_DTYPE_FP8_E4M3}
 
 
-@dataclasses.dataclass
+@dataclasses.dataclass(slots=True)
 class Norm:
     y: torch.Tensor
     y_scales: torch.Tensor | None
@@ -524,7 +524,7 @@ def _norm_args(fn, x, weight, kind):
     if dt not in _ROW_TYPES:
         raise ValueError(f"{fn}: rows must be float32 or bfloat16 (got {dt})")
     index = x.get_device()
-    return shape, dt, index, code, _tensor(fn, "weight", weight, shape[1:], _ROW_TYPES, index)
+    return shape, dt, index, code, _tensor(fn, "weight", weight, (shape[1],), _ROW_TYPES, index)
 
 
 def moe_norm(x, weight, bias=None, residual=None, kind="layer", eps=1e-5, out_dtype=None, y=None, y_scales=None,
@@ -539,7 +539,7 @@ def moe_norm(x, weight, bias=None, residual=None, kind="layer", eps=1e-5, out_dt
     T, H = shape
     x_ptr, ldx = _rows(fn, "x", x, shape, dt, index)
     r_ptr, ldr = (None, 0) if residual is None else _rows(fn, "residual", residual, shape, dt, index)
-    b_ptr = None if bias is None else _tensor(fn, "bias", bias, weight.shape, (weight.dtype,), index)
+    b_ptr = None if bias is None else _tensor(fn, "bias", bias, (H,), (weight.dtype,), index)
     if y is not None and out_dtype is not None and y.dtype != out_dtype:
         raise ValueError(f"{fn}: y has dtype {y.dtype}, not {out_dtype}")
     yt = y.dtype if y is not None else out_dtype or dt
@@ -567,9 +567,9 @@ def moe_norm(x, weight, bias=None, residual=None, kind="layer", eps=1e-5, out_dt
             if rstd is None:
                 rstd = torch.empty(T, dtype=torch.float32, device=dev)
     y_ptr = _tensor(fn, "y", y, shape, (yt,), index)
-    rstd_ptr = _tensor(fn, "rstd", rstd, shape[:1], _F32, index)
+    rstd_ptr = _tensor(fn, "rstd", rstd, (T,), _F32, index)
     ys_ptr = _tensor(fn, "y_scales", y_scales, (T, H // 128), _F32, index) if fp8 else None
-    mean_ptr = _tensor(fn, "mean", mean, shape[:1], _F32, index) if layer else None
+    mean_ptr = _tensor(fn, "mean", mean, (T,), _F32, index) if layer else None
     sum_ptr = None if residual is None else _tensor(fn, "sum", sum, shape, (dt,), index)
     st = lib.moe_norm(x_ptr, ldx, r_ptr, ldr, _CODES[dt], T, H, code, w_ptr, b_ptr, _CODES[weight.dtype], eps,
                       sum_ptr, y_ptr, ys_ptr, _CODES[yt], mean_ptr, rstd_ptr, _stream(stream, index))
@@ -600,8 +600,8 @@ def moe_norm_backward(dy, rows, weight, mean, rstd, kind="layer", dsum=None, wan
     ds_ptr, ld_ds = (None, 0) if dsum is None else _rows(fn, "dsum", dsum, shape, dt, index)
     if layer and mean is None:
         raise ValueError(f"{fn}: kind 'layer' needs the rows' means")
-    mean_ptr = _tensor(fn, "mean", mean, shape[:1], _F32, index) if layer else None
-    rstd_ptr = _tensor(fn, "rstd", rstd, shape[:1], _F32, index)
+    mean_ptr = _tensor(fn, "mean", mean, (T,), _F32, index) if layer else None
+    rstd_ptr = _tensor(fn, "rstd", rstd, (T,), _F32, index)
     if _elsewhere(fn, index, stream):
         with torch.cuda.device(index):
             return moe_norm_backward(dy, rows, weight, mean, rstd, kind, dsum, want_bias, out, workspace, stream)
@@ -615,10 +615,10 @@ def moe_norm_backward(dy, rows, weight, mean, rstd, kind="layer", dsum=None, wan
             if workspace is None:
                 workspace = torch.empty(moe_norm_backward_workspace_bytes(T, H), dtype=torch.uint8, device=dev)
     dx_ptr = _tensor(fn, "dx", out["dx"], shape, (dt,), index)
-    dw_ptr = _tensor(fn, "dweight", out["dweight"], shape[1:], _F32, index)
+    dw_ptr = _tensor(fn, "dweight", out["dweight"], (H,), _F32, index)
     if want_bias and out.get("dbias") is None:
         raise ValueError(f"{fn}: want_bias needs out['dbias']")
-    db_ptr = _tensor(fn, "dbias", out["dbias"], shape[1:], _F32, index) if want_bias else None
+    db_ptr = _tensor(fn, "dbias", out["dbias"], (H,), _F32, index) if want_bias else None
     ws_ptr, ws_bytes = _workspace(fn, workspace, index)
     st = lib.moe_norm_backward(dy_ptr, ld_dy, s_ptr, ld_s, ds_ptr, ld_ds, _CODES[dt], T, H, code, w_ptr,
                                _CODES[weight.dtype], mean_ptr, rstd_ptr, dx_ptr, dw_ptr, db_ptr, ws_ptr, ws_bytes,

@@ -51,6 +51,7 @@ struct BwdArgs {
   const float *mean, *rstd;
   uint8_t* dx;
   float* part;  // [2][G][H]: weight partials, then bias partials
+  float *dw, *db;  // where one workgroup is all: the results themselves
 };
 
 // 16 bytes of a row (VEC = 16 / ESZ elements), at the elements' own alignment: one wide access, which the memory system
@@ -355,7 +356,7 @@ __global__ __launch_bounds__((TPR < 256 ? 256 : TPR)) void norm_bwd_kernel(const
   // one partial row per workgroup: the row groups of a wavefront are added by lane exchanges, the wavefronts in LDS
 #pragma unroll
   for (int k = 0; k < (BIAS ? 2 : 1); ++k) {
-    float* out = a.part + ((int64_t)k * gridDim.x + blockIdx.x) * a.H;
+    float* out = gridDim.x == 1 ? (k == 0 ? a.dw : a.db) : a.part + ((int64_t)k * gridDim.x + blockIdx.x) * a.H;
     float v[NV][VEC];
 #pragma unroll
     for (int i = 0; i < NV; ++i)
@@ -473,6 +474,7 @@ int norm_backward_groups(int64_t T, int H) {
   const int tpr = norm::threads_per_row(H);
   const int64_t most = tpr <= 256 ? 512 : 256;
   const int64_t need = (T + rpb - 1) / rpb;
+  if (T > 0 && need <= 4) return 1;  // a few passes of one workgroup cost less than a second launch
   int64_t g = need / 4;
   if (g < 256) g = need < 256 ? need : 256;
   return (int)(g < most ? g : most);
@@ -525,6 +527,8 @@ void launch_norm_backward(const NormLaunch& p, hipStream_t s) {
   a.rstd = p.rstd;
   a.dx = (uint8_t*)p.dx;
   a.part = p.part;
+  a.dw = p.dweight;
+  a.db = p.dbias;
   const int tpr = norm::threads_per_row(p.H);
   const int G = norm_backward_groups(p.T, p.H);
   if (G > 0) {
@@ -534,6 +538,7 @@ void launch_norm_backward(const NormLaunch& p, hipStream_t s) {
     else
       bias ? norm::launch_shape<2, norm::BWD_BIAS>(a, tpr, G, s) : norm::launch_shape<2, norm::BWD>(a, tpr, G, s);
   }
+  if (G == 1) return;  // it has written the sums themselves
   hipLaunchKernelGGL(norm::norm_reduce_kernel, dim3((unsigned)((p.H + 31) / 32), p.dbias != nullptr ? 2 : 1),
                      dim3(256), 0, s, p.part, G, p.H, p.dweight, p.dbias);
 }
