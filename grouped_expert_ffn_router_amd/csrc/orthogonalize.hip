@@ -6,7 +6,7 @@
 // each is stored twice, once transposed: p^2 q + p^3 + 2 p^2 q operations a step instead of 2 p^2 q + 2 p^3 + 2 p^2 q.
 // Bound by the matrix instructions: a step at p = 2048, q = 7168 is 99 GFLOP on 59 MB.  A product whose tiles do not fill
 // the last round of the 256 compute units shares those tiles' reductions among workgroups and joins them in a launch of its
-// own (8 x 2048 x 7168: 288 tiles of 256 x 256, X X^T from 369 to 264 + 14 us); see shape().
+// own (8 x 2048 x 7168: 288 tiles of 256 x 256, X X^T from 369 to 251 + 11 us); see shape().
 //
 // Number formats.  Operands are fp16 (11 bits; the products then run at the bf16 rate with an eighth of its rounding
 // error), accumulated in fp32.  Everything carries a factor S = 2^12: entries of an orthogonal-like p x q matrix are near
@@ -21,10 +21,11 @@
 // SPLIT (fp32 outputs, and bf16 outputs of matrices so small that the launches are what is paid for) gives hi and lo to the
 // operands too and sums lo hi + hi lo + hi hi: three products, the same tiles.
 //
-// Layout: X [P][Q] hi and lo, its transpose [Q][P] (two, used in turn: a step's tiles read one and write the other), A and
-// B [P][P]; P and Q are p and q rounded up to the tile size and zero-filled, which the iteration keeps, so no product has
-// a bound to check.  Every product is C[i][j] = sum_k M[i][k] N[j][k] with both reductions contiguous: X X^T from X
-// twice, A A from A twice (symmetric), B X from B and the transpose of X.
+// Layout: X is held transposed only, X^T [Q][P] (two, used in turn: an update's tiles read one and write the other; lo in
+// place where it is no operand), A and B [P][P]; P and Q are p and q rounded up to the tile size and zero-filled, which the
+// iteration keeps, so no product has a bound to check.  a sits on B's diagonal: X^T <- X^T (a + b A + c A A) + a lo.  A A and
+// X^T B reduce along rows of both operands; X X^T reduces over the rows of X^T, through the transposing LDS load.  Holding X
+// in both orientations instead cost an update 10 bytes per value for 6 (8 x 2048 x 7168: 615 us for 494).
 #include <utility>
 
 #include "common.h"
@@ -564,9 +565,9 @@ __global__ __launch_bounds__(256) void join_kernel(const Args a) {
 }
 
 // Sides of at most 128 (P = 64 or 128): B = a + b A + c A A and X^T <- X^T B in one launch.  A workgroup makes the 64
-// rows of B that its 64 x 64 tile of X^T needs from all of A in LDS (twice the tile's own work at P = 128, but nothing to wait
-// for), which saves the launch between the two products.  Small batches are bound by launches: 8 x 128 x 256 in fp32 takes
-// 80 us with three launches a step.
+// rows of B that its 64 x 64 tile needs from all of A in LDS (twice the tile's own work at P = 128, but nothing to wait for),
+// which saves the launch between the two products.  Small batches are bound by launches, 4 to 6 us each: 8 x 128 x 256 in
+// fp32 takes 64 us with 12 of them and took 75 us with 17; plan_of() has the other side.
 template <int MODE, int P, bool SPLIT>
 __global__ __launch_bounds__(256) void narrow_kernel(const Args a, const uint8_t* A0, const uint8_t* A1, int64_t a_batch,
                                                      bool b_first, float pa, float pb, float pc) {

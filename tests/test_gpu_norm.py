@@ -301,6 +301,21 @@ def test_no_rows():
     assert (out["dweight"] == 0).all() and (out["dbias"] == 0).all()
 
 
+@pytest.mark.parametrize("T,H", [(1, 64), (64, 128), (65, 128), (300, 1000), (9, 5000), (700, 2048), (33, 20000)])
+def test_workspace_is_enough(T, H):
+    x, w, b, _ = inputs(T, H, torch.bfloat16, torch.bfloat16, True, False)
+    f = m.moe_norm(x, w, b)
+    dy = normal(60, T, H).bfloat16()
+    need = m.moe_norm_backward_workspace_bytes(T, H)
+    outs = []
+    for fill in (0, 255):
+        buf = torch.full((need + 4096,), fill, dtype=torch.uint8, device="cuda")
+        outs.append(m.moe_norm_backward(dy, x, w, f.mean, f.rstd, workspace=buf[:need]))
+        assert (buf[need:] == fill).all()
+    assert all(torch.equal(outs[0][k], outs[1][k]) for k in outs[0])
+    check_backward(outs[0], dy, x, w, f.mean, f.rstd, "layer", None)
+
+
 def test_other_stream_and_two_calls():
     """Calls on two streams at once, each with its own workspace, give the results of one after the other."""
     T, H = 700, 2048

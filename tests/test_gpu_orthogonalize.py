@@ -168,6 +168,24 @@ def test_canaries_repeats_and_unaligned():
     check(o, definition(flip))
 
 
+@pytest.mark.parametrize("B,mm,n,dt", [(2, 60, 300, torch.float32), (8, 128, 256, torch.bfloat16),
+                                       (20, 128, 2000, torch.float32), (3, 1001, 333, torch.float32),
+                                       (4, 512, 512, torch.bfloat16), (1, 1536, 2100, torch.bfloat16),
+                                       (9, 1300, 1000, torch.bfloat16), (5, 1100, 1030, torch.float32)])
+def test_workspace_is_enough(B, mm, n, dt):
+    """The bytes behind the workspace stay, and the result does not depend on what the workspace held."""
+    g = normal(8, B, mm, n)
+    need = m.moe_orthogonalize_workspace_bytes(B, mm, n, dt)
+    assert need % 256 == 0
+    outs = []
+    for fill in (0, 255):
+        buf = torch.full((need + 4096,), fill, dtype=torch.uint8, device="cuda")
+        outs.append(m.moe_orthogonalize(g, out_dtype=dt, workspace=buf[:need]))
+        assert (buf[need:] == fill).all()
+    assert torch.equal(*outs)
+    check(outs[0], definition(g))
+
+
 def test_batches_are_independent():
     g = normal(6, 6, 150, 140)
     a = m.moe_orthogonalize(g)
