@@ -696,7 +696,7 @@ moe_status moe_norm(const void* x, int64_t ldx, const void* residual, int64_t ld
 
 size_t moe_norm_backward_workspace_bytes(int64_t T, int32_t H) {
   if (T < 0 || T >= (1ll << 31) || H < 1 || H > 65536) return 0;
-  return align256(2 * (size_t)norm_backward_groups(T, H) * (size_t)H * sizeof(float)) + 256;
+  return align256(norm_backward_floats(T, H) * sizeof(float)) + 256;
 }
 
 moe_status moe_norm_backward(const void* dy, int64_t ld_dy, const void* s, int64_t ld_s, const void* dsum,

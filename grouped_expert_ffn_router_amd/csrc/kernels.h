@@ -96,9 +96,9 @@ struct NormLaunch {
   int64_t ld_dy;
   void* dx;
   float *dweight, *dbias;
-  float* part;  // workspace: [2][norm_backward_groups][H]
+  float* part;  // workspace: norm_backward_floats
 };
-int norm_backward_groups(int64_t T, int H);
+size_t norm_backward_floats(int64_t T, int H);
 void launch_norm(const NormLaunch& p, hipStream_t s);
 void launch_norm_backward(const NormLaunch& p, hipStream_t s);
 

@@ -7,8 +7,8 @@
 //
 // Bound by memory: forward reads x (and residual) and writes y (and s) once, backward reads dy and s (and dsum) and
 // writes ds once; a row stays in registers between its statistics and its result.  TPR threads share a row, 16
-// columns each (TPR = 16 .. 1024 by powers of two; rows above 16384 columns take 64 per thread), so a thread has two
-// to four 16-byte loads of each operand in flight and the two sums of a row cost one or two exchanges: in a wavefront
+// columns each (TPR = 16 .. 1024 by powers of two; forward rows above 16384 columns take 64 per thread, wide backward ones a
+// form of their own), so a thread has two to four 16-byte loads of each operand in flight and the two sums of a row cost one or two exchanges: in a wavefront
 // by lane shuffles, across wavefronts through LDS.  Rows of any width, stride and alignment take the same 16-byte
 // accesses, at the element's alignment; only a row's last few elements go one by one.
 // Statistics: the mean first, then the squares of the differences, both in fp32 from registers: no cancellation of
@@ -17,6 +17,9 @@
 // The weight's gradient: a persistent grid of G workgroups walks the rows, each thread keeping its columns' sums in
 // fp32 registers; the groups of a workgroup are added through LDS, each workgroup writes one partial row, and a second
 // launch adds the G partial rows in a fixed order.  No atomics: results do not change from run to run.
+//
+// Measured, 16384 x 4096 bf16: forward 53 us (5.1 TB/s), backward with both parameters' gradients 81 us (5.0 TB/s), where a
+// device copy of that size runs at 5.4 TB/s.
 #include "common.h"
 #include "kernels.h"
 
@@ -52,6 +55,7 @@ struct BwdArgs {
   uint8_t* dx;
   float* part;  // [2][G][H]: weight partials, then bias partials
   float *dw, *db;  // where one workgroup is all: the results themselves
+  float* sums;     // wide rows: [T][2], mean(t) and mean(t z)
 };
 
 // 16 bytes of a row (VEC = 16 / ESZ elements), at the elements' own alignment: one wide access, which the memory system
@@ -392,6 +396,96 @@ __global__ __launch_bounds__((TPR < 256 ? 256 : TPR)) void norm_bwd_kernel(const
   }
 }
 
+// Wide rows: a thread would hold more columns' sums than it has registers (with them spilled, 3640 x 18432 took 3.3 ms; this
+// form takes 0.14).  The rows' two sums in a launch of their own, then the rest column by column: five passes over
+// rows instead of three.
+template <int ESZ, bool TAIL>
+__global__ __launch_bounds__(256) void norm_bwd_sums_kernel(const BwdArgs a) {
+  constexpr int VEC = 16 / ESZ;
+  __shared__ float red[2][8];
+  int flip = 0;
+  const int64_t row = blockIdx.x;
+  const float m = a.rms ? 0.0f : a.mean[row], r = a.rstd[row];
+  float c12[2] = {0.0f, 0.0f};
+#pragma unroll 2
+  for (int c = (int)threadIdx.x * VEC; c < a.H; c += 256 * VEC) {
+    const i32x4_t qy = load_row16<ESZ, TAIL>(a.dy + row * a.ld_dy * ESZ, c, a.H);
+    const i32x4_t qs = load_row16<ESZ, TAIL>(a.s + row * a.ld_s * ESZ, c, a.H);
+    float w[VEC];
+    load_param<VEC, TAIL>(a.w, a.w_bf16, c, a.H, w);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      const bool in = !TAIL || c + e < a.H;
+      const float z = in ? (element<ESZ>(qs, e) - m) * r : 0.0f;
+      const float tw = element<ESZ>(qy, e) * w[e];
+      c12[0] += tw;
+      c12[1] = __builtin_fmaf(tw, z, c12[1]);
+    }
+  }
+  row_sum<256, 256, 2>(c12, red, flip);
+  if (threadIdx.x == 0) {
+    a.sums[2 * row] = a.rms ? 0.0f : c12[0] / (float)a.H;
+    a.sums[2 * row + 1] = c12[1] / (float)a.H;
+  }
+}
+
+constexpr int SPAN = 4096;  // columns of a workgroup of the kernel below
+
+// blockIdx.x: column span, blockIdx.y: row group; one partial row span per workgroup
+template <int ESZ, bool TAIL, bool BIAS>
+__global__ __launch_bounds__(256) void norm_bwd_span_kernel(const BwdArgs a) {
+  constexpr int VEC = 16 / ESZ, NV = ESZ;
+  const int c0 = blockIdx.x * SPAN, G = gridDim.y;
+  float dw[NV][VEC], db[BIAS ? NV : 1][VEC], w[NV][VEC];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      dw[i][e] = 0.0f;
+      if constexpr (BIAS) db[i][e] = 0.0f;
+      w[i][e] = 0.0f;
+    }
+    const int c = c0 + (i * 256 + (int)threadIdx.x) * VEC;
+    load_param<VEC, TAIL>(a.w, a.w_bf16, c, a.H, w[i]);
+  }
+  for (int64_t row = blockIdx.y; row < a.T; row += G) {
+    const float m = a.rms ? 0.0f : a.mean[row], r = a.rstd[row], c1 = a.sums[2 * row], c2 = a.sums[2 * row + 1];
+    i32x4_t qy[NV], qs[NV], qd[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = c0 + (i * 256 + (int)threadIdx.x) * VEC;
+      qy[i] = load_row16<ESZ, TAIL>(a.dy + row * a.ld_dy * ESZ, c, a.H);
+      qs[i] = load_row16<ESZ, TAIL>(a.s + row * a.ld_s * ESZ, c, a.H);
+      if (a.dsum != nullptr) qd[i] = load_row16<ESZ, TAIL>(a.dsum + row * a.ld_dsum * ESZ, c, a.H);
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = c0 + (i * 256 + (int)threadIdx.x) * VEC;
+      float d[VEC];
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const bool in = c + (TAIL ? e : 0) < a.H;
+        const float dy = element<ESZ>(qy[i], e), z = in ? (element<ESZ>(qs[i], e) - m) * r : 0.0f;
+        dw[i][e] = __builtin_fmaf(dy, z, dw[i][e]);
+        if constexpr (BIAS) db[i][e] += dy;
+        d[e] = (dy * w[i][e] - c1 - z * c2) * r;
+        if (a.dsum != nullptr) d[e] += element<ESZ>(qd[i], e);
+      }
+      store_row16<ESZ, TAIL, VEC>(a.dx + row * a.H * ESZ, c, a.H, d);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < (BIAS ? 2 : 1); ++k) {
+    float* out = a.part + ((int64_t)k * G + blockIdx.y) * a.H;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int d = 0; d < VEC / 4; ++d)
+        store_row16<4, TAIL, 4>(reinterpret_cast<uint8_t*>(out), c0 + (i * 256 + (int)threadIdx.x) * VEC + 4 * d, a.H,
+                                reinterpret_cast<const float(&)[4]>((k == 0 ? dw[i] : db[BIAS ? i : 0])[4 * d]));
+  }
+}
+
 // out[c] = sum over the G partial rows, in a fixed order: 32 columns (8 threads of 4) and 32 row lanes per workgroup.
 // blockIdx.y: 0 the weight's partials, 1 the bias's.  G = 0 (no rows) writes zeros.
 __global__ __launch_bounds__(256) void norm_reduce_kernel(const float* __restrict__ part, int G, int H,
@@ -431,6 +525,15 @@ static int rows_per_block(int H) {
 
 enum Kind { FWD, BWD, BWD_BIAS };
 
+// Whether the backward pass takes the form of wide rows.  Up to 8192 columns a thread holds its 16 columns' sums and row
+// (4.9 to 5.1 TB/s); of 1024 threads each has half the registers, which bf16 rows without a bias's sums fit (3.4 to 3.8 TB/s
+// up to 16384 columns) and others spill out of (1.2 to 2.3); the form of wide rows runs at 2.8 whatever the width.
+static bool wide(int H, bool f32, bool bias) { return H > 16384 || (H > 8192 && (f32 || bias)); }
+static int64_t wide_groups(int64_t T, int H) {
+  const int64_t most = 1024 / ((H + SPAN - 1) / SPAN);
+  return T < most ? T : most;
+}
+
 template <int ESZ, Kind KIND, bool TAIL, int NV, int TPR, typename Args>
 static void launch_tail(const Args& a, unsigned grid, hipStream_t s) {
   constexpr int TH = TPR < 256 ? 256 : TPR;
@@ -451,16 +554,28 @@ static void launch_tpr(const Args& a, unsigned grid, hipStream_t s) {
 template <int ESZ, Kind KIND, typename Args>
 static void launch_shape(const Args& a, int tpr, unsigned grid, hipStream_t s) {
   constexpr int NV = ESZ;  // 16 columns per thread
-  if (a.H > 16384) return launch_tpr<ESZ, KIND, 4 * NV, 1024>(a, grid, s);
+  if constexpr (KIND == FWD)
+    if (a.H > 16384) return launch_tpr<ESZ, KIND, 4 * NV, 1024>(a, grid, s);
+  if constexpr (KIND == FWD || (KIND == BWD && ESZ == 2))  // else wide()
+    if (tpr == 1024) return launch_tpr<ESZ, KIND, NV, 1024>(a, grid, s);
   switch (tpr) {
     case 16: return launch_tpr<ESZ, KIND, NV, 16>(a, grid, s);
     case 32: return launch_tpr<ESZ, KIND, NV, 32>(a, grid, s);
     case 64: return launch_tpr<ESZ, KIND, NV, 64>(a, grid, s);
     case 128: return launch_tpr<ESZ, KIND, NV, 128>(a, grid, s);
     case 256: return launch_tpr<ESZ, KIND, NV, 256>(a, grid, s);
-    case 512: return launch_tpr<ESZ, KIND, NV, 512>(a, grid, s);
-    default: return launch_tpr<ESZ, KIND, NV, 1024>(a, grid, s);
+    default: return launch_tpr<ESZ, KIND, NV, 512>(a, grid, s);
   }
+}
+
+template <int ESZ, bool TAIL>
+static void launch_wide(const BwdArgs& a, bool bias, int G, hipStream_t s) {
+  hipLaunchKernelGGL((norm_bwd_sums_kernel<ESZ, TAIL>), dim3((unsigned)a.T), dim3(256), 0, s, a);
+  const dim3 grid((unsigned)((a.H + SPAN - 1) / SPAN), (unsigned)G);
+  if (bias)
+    hipLaunchKernelGGL((norm_bwd_span_kernel<ESZ, TAIL, true>), grid, dim3(256), 0, s, a);
+  else
+    hipLaunchKernelGGL((norm_bwd_span_kernel<ESZ, TAIL, false>), grid, dim3(256), 0, s, a);
 }
 
 }  // namespace norm
@@ -469,7 +584,8 @@ static void launch_shape(const Args& a, int tpr, unsigned grid, hipStream_t s) {
 // while a row is summed that many keep the memory busy, and the partial rows stay a few percent of the traffic
 // (16384 x 4096 bf16 with bias: 512 workgroups 81 us, 1024 95 us, 256 128 us).  And no more than leaves each four passes
 // over its rows (2048 x 4096: 512 workgroups 18.5 us, 1024 19.8 us), but at least one per compute unit.
-int norm_backward_groups(int64_t T, int H) {
+static int backward_groups(int64_t T, int H, bool wide) {
+  if (wide) return (int)norm::wide_groups(T, H);
   const int rpb = norm::rows_per_block(H);
   const int tpr = norm::threads_per_row(H);
   const int64_t most = tpr <= 256 ? 512 : 256;
@@ -478,6 +594,14 @@ int norm_backward_groups(int64_t T, int H) {
   int64_t g = need / 4;
   if (g < 256) g = need < 256 ? need : 256;
   return (int)(g < most ? g : most);
+}
+
+// Partial rows, and for wide rows the sums of every row: what the larger of the forms that rows of H columns can take needs.
+size_t norm_backward_floats(int64_t T, int H) {
+  const size_t held = norm::wide(H, false, false) ? 0 : 2 * (size_t)backward_groups(T, H, false) * (size_t)H;
+  const size_t wide =
+      norm::wide(H, true, true) ? 2 * (size_t)backward_groups(T, H, true) * (size_t)H + 2 * (size_t)T : 0;
+  return held > wide ? held : wide;
 }
 
 void launch_norm(const NormLaunch& p, hipStream_t s) {
@@ -530,15 +654,22 @@ void launch_norm_backward(const NormLaunch& p, hipStream_t s) {
   a.dw = p.dweight;
   a.db = p.dbias;
   const int tpr = norm::threads_per_row(p.H);
-  const int G = norm_backward_groups(p.T, p.H);
-  if (G > 0) {
-    const bool f32 = p.dtype == MOE_DTYPE_F32, bias = p.dbias != nullptr;
+  const bool f32 = p.dtype == MOE_DTYPE_F32, bias = p.dbias != nullptr, wide = norm::wide(p.H, f32, bias);
+  const int G = backward_groups(p.T, p.H, wide);
+  if (G > 0 && wide) {
+    a.sums = p.part + 2 * (size_t)G * p.H;
+    const bool tail = p.H % (f32 ? 4 : 8) != 0;
+    if (f32)
+      tail ? norm::launch_wide<4, true>(a, bias, G, s) : norm::launch_wide<4, false>(a, bias, G, s);
+    else
+      tail ? norm::launch_wide<2, true>(a, bias, G, s) : norm::launch_wide<2, false>(a, bias, G, s);
+  } else if (G > 0) {
     if (f32)
       bias ? norm::launch_shape<4, norm::BWD_BIAS>(a, tpr, G, s) : norm::launch_shape<4, norm::BWD>(a, tpr, G, s);
     else
       bias ? norm::launch_shape<2, norm::BWD_BIAS>(a, tpr, G, s) : norm::launch_shape<2, norm::BWD>(a, tpr, G, s);
   }
-  if (G == 1) return;  // it has written the sums themselves
+  if (G == 1 && !wide) return;  // it has written the sums themselves
   hipLaunchKernelGGL(norm::norm_reduce_kernel, dim3((unsigned)((p.H + 31) / 32), p.dbias != nullptr ? 2 : 1),
                      dim3(256), 0, s, p.part, G, p.H, p.dweight, p.dbias);
 }

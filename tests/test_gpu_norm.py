@@ -84,6 +84,10 @@ CASES = [  # T, H, rows, weights, kind, bias, residual
     (66, 5120, torch.bfloat16, torch.float32, "layer", True, False),
     (20, 8192, torch.float32, torch.float32, "rms", False, True),
     (7, 12289, torch.bfloat16, torch.bfloat16, "layer", True, False),
+    (600, 9000, torch.float32, torch.bfloat16, "layer", True, True),
+    (9, 16381, torch.bfloat16, torch.float32, "rms", False, True),
+    (3, 10240, torch.float32, torch.float32, "rms", False, True),
+    (500, 17000, torch.bfloat16, torch.float32, "layer", True, True),
     (9, 16384, torch.bfloat16, torch.bfloat16, "rms", False, True),
     (3, 16392, torch.bfloat16, torch.bfloat16, "layer", True, True),
     (2, 65536, torch.float32, torch.float32, "layer", True, False),
@@ -301,7 +305,7 @@ def test_no_rows():
     assert (out["dweight"] == 0).all() and (out["dbias"] == 0).all()
 
 
-@pytest.mark.parametrize("T,H", [(1, 64), (64, 128), (65, 128), (300, 1000), (9, 5000), (700, 2048), (33, 20000)])
+@pytest.mark.parametrize("T,H", [(1, 64), (64, 128), (65, 128), (300, 1000), (9, 5000), (700, 2048), (33, 20000), (40, 12000)])
 def test_workspace_is_enough(T, H):
     x, w, b, _ = inputs(T, H, torch.bfloat16, torch.bfloat16, True, False)
     f = m.moe_norm(x, w, b)
