@@ -7,8 +7,8 @@
 //
 // Bound by memory: forward reads x (and residual) and writes y (and s) once, backward reads dy and s (and dsum) and
 // writes ds once; a row stays in registers between its statistics and its result.  TPR threads share a row, 16
-// columns each (TPR = 16 .. 1024 by powers of two; forward rows above 16384 columns take 64 per thread, wide backward ones a
-// form of their own), so a thread has two to four 16-byte loads of each operand in flight and the two sums of a row cost one or two exchanges: in a wavefront
+// columns each (TPR = 16 .. 1024 by powers of two; forward bf16 rows 24 where fewer threads then idle, above 16384 columns
+// 64, wide backward ones a form of their own), so a thread has two to four 16-byte loads of each operand in flight and the two sums of a row cost one or two exchanges: in a wavefront
 // by lane shuffles, across wavefronts through LDS.  Rows of any width, stride and alignment take the same 16-byte
 // accesses, at the element's alignment; only a row's last few elements go one by one.
 // Statistics: the mean first, then the squares of the differences, both in fp32 from registers: no cancellation of
@@ -523,6 +523,14 @@ static int rows_per_block(int H) {
   return t < 256 ? 256 / t : 1;
 }
 
+// The forward pass of bf16 rows: half the threads with 24 columns each where that holds the row, so that fewer of them have
+// none (2304 columns 4.7 -> 5.4 TB/s, 5120 4.8 -> 5.4, 9216 4.35 -> 5.3; fp32 rows, whose threads have four loads each
+// already, lose: 5120 5.1 -> 4.9)
+static int forward_threads_per_row(int H, bool f32) {
+  const int t = threads_per_row(H);
+  return !f32 && t >= 128 && H <= 12 * t ? t / 2 : t;
+}
+
 enum Kind { FWD, BWD, BWD_BIAS };
 
 // Whether the backward pass takes the form of wide rows.  Up to 8192 columns a thread holds its 16 columns' sums and row
@@ -556,6 +564,15 @@ static void launch_shape(const Args& a, int tpr, unsigned grid, hipStream_t s) {
   constexpr int NV = ESZ;  // 16 columns per thread
   if constexpr (KIND == FWD)
     if (a.H > 16384) return launch_tpr<ESZ, KIND, 4 * NV, 1024>(a, grid, s);
+  if constexpr (KIND == FWD && ESZ == 2)
+    if (a.H > 16 * tpr) {  // forward_threads_per_row(): 24 columns per thread
+      switch (tpr) {
+        case 64: return launch_tpr<ESZ, KIND, 3, 64>(a, grid, s);
+        case 128: return launch_tpr<ESZ, KIND, 3, 128>(a, grid, s);
+        case 256: return launch_tpr<ESZ, KIND, 3, 256>(a, grid, s);
+        default: return launch_tpr<ESZ, KIND, 3, 512>(a, grid, s);
+      }
+    }
   if constexpr (KIND == FWD || (KIND == BWD && ESZ == 2))  // else wide()
     if (tpr == 1024) return launch_tpr<ESZ, KIND, NV, 1024>(a, grid, s);
   switch (tpr) {
@@ -623,8 +640,8 @@ void launch_norm(const NormLaunch& p, hipStream_t s) {
   a.ys = p.y_scales;
   a.mean = p.mean;
   a.rstd = p.rstd;
-  int tpr = norm::threads_per_row(p.H);
   const bool f32 = p.dtype == MOE_DTYPE_F32;
+  int tpr = norm::forward_threads_per_row(p.H, f32);
   if (p.y_fp8 && f32 && tpr < 32) tpr = 32;  // a 128-column block of fp32 rows spans 32 lanes
   const int rpb = tpr < 256 ? 256 / tpr : 1;
   const unsigned grid = (unsigned)((p.T + rpb - 1) / rpb);

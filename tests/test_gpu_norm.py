@@ -86,6 +86,10 @@ CASES = [  # T, H, rows, weights, kind, bias, residual
     (7, 12289, torch.bfloat16, torch.bfloat16, "layer", True, False),
     (600, 9000, torch.float32, torch.bfloat16, "layer", True, True),
     (9, 16381, torch.bfloat16, torch.float32, "rms", False, True),
+    (21, 1111, torch.bfloat16, torch.bfloat16, "layer", True, True),
+    (30, 3000, torch.bfloat16, torch.float32, "layer", True, False),
+    (11, 6144, torch.bfloat16, torch.bfloat16, "rms", False, True),
+    (5, 9216, torch.bfloat16, torch.bfloat16, "layer", True, True),
     (3, 10240, torch.float32, torch.float32, "rms", False, True),
     (500, 17000, torch.bfloat16, torch.float32, "layer", True, True),
     (9, 16384, torch.bfloat16, torch.bfloat16, "rms", False, True),
@@ -112,7 +116,8 @@ def test_forward(T, H, dt, wdt, kind, bias, residual):
 @pytest.mark.parametrize("T,H,dt,kind,bias,residual", [
     (1, 128, torch.bfloat16, "rms", False, False), (37, 128, torch.float32, "layer", True, True),
     (130, 384, torch.bfloat16, "layer", True, True), (64, 7168, torch.bfloat16, "rms", False, True),
-    (19, 2176, torch.float32, "rms", False, False), (3, 16512, torch.bfloat16, "layer", True, False),
+    (19, 2176, torch.float32, "rms", False, False), (12, 5120, torch.bfloat16, "layer", True, True),
+    (3, 16512, torch.bfloat16, "layer", True, False),
     (2, 32896, torch.float32, "rms", False, True)])
 @pytest.mark.parametrize("code", [torch.uint8, torch.float8_e4m3fn])
 def test_forward_to_e4m3(T, H, dt, kind, bias, residual, code):
