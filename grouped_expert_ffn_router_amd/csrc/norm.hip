@@ -518,25 +518,25 @@ static int threads_per_row(int H) {
   while (t < 1024 && t * 16 < H) t *= 2;
   return t;
 }
-static int rows_per_block(int H) {
+// bf16 rows: half the threads with 24 columns each where that holds the row and leaves fewer threads without any.  Forward
+// (2304 columns 4.7 -> 5.4 TB/s, 5120 4.8 -> 5.4, 9216 4.35 -> 5.3) whenever it does; backward, which has half as many
+// wavefronts then, up to 5/8 of the width (2304 columns 4.0 -> 5.1 TB/s, 4608 4.8 -> 5.1; 6144 loses, 5.3 -> 4.9), and
+// instead of 1024 threads always (9216 3.4 -> 5.1).  fp32 rows, whose threads have four loads each already, lose (forward,
+// 5120 5.1 -> 4.9).
+static int threads_per_row(int H, bool f32, bool backward) {
   const int t = threads_per_row(H);
-  return t < 256 ? 256 / t : 1;
-}
-
-// The forward pass of bf16 rows: half the threads with 24 columns each where that holds the row, so that fewer of them have
-// none (2304 columns 4.7 -> 5.4 TB/s, 5120 4.8 -> 5.4, 9216 4.35 -> 5.3; fp32 rows, whose threads have four loads each
-// already, lose: 5120 5.1 -> 4.9)
-static int forward_threads_per_row(int H, bool f32) {
-  const int t = threads_per_row(H);
-  return !f32 && t >= 128 && H <= 12 * t ? t / 2 : t;
+  return !f32 && t >= 128 && H <= (backward && t < 1024 ? 10 : 12) * t ? t / 2 : t;
 }
 
 enum Kind { FWD, BWD, BWD_BIAS };
 
-// Whether the backward pass takes the form of wide rows.  Up to 8192 columns a thread holds its 16 columns' sums and row
-// (4.9 to 5.1 TB/s); of 1024 threads each has half the registers, which bf16 rows without a bias's sums fit (3.4 to 3.8 TB/s
-// up to 16384 columns) and others spill out of (1.2 to 2.3); the form of wide rows runs at 2.8 whatever the width.
-static bool wide(int H, bool f32, bool bias) { return H > 16384 || (H > 8192 && (f32 || bias)); }
+// Whether the backward pass takes the form of wide rows.  512 threads hold rows of up to 8192 columns (bf16: 12288) with
+// their sums in registers (4.5 to 5.1 TB/s); of 1024 threads each has half the registers, which bf16 rows without a bias's
+// sums fit (3.8 TB/s at 16384 columns) and others spill out of (1.2 to 2.3); the form of wide rows runs at 2.8 whatever the
+// width.
+static bool wide(int H, bool f32, bool bias) {
+  return H > 16384 || (H > 8192 && f32) || (H > 12288 && bias);
+}
 static int64_t wide_groups(int64_t T, int H) {
   const int64_t most = 1024 / ((H + SPAN - 1) / SPAN);
   return T < most ? T : most;
@@ -564,8 +564,8 @@ static void launch_shape(const Args& a, int tpr, unsigned grid, hipStream_t s) {
   constexpr int NV = ESZ;  // 16 columns per thread
   if constexpr (KIND == FWD)
     if (a.H > 16384) return launch_tpr<ESZ, KIND, 4 * NV, 1024>(a, grid, s);
-  if constexpr (KIND == FWD && ESZ == 2)
-    if (a.H > 16 * tpr) {  // forward_threads_per_row(): 24 columns per thread
+  if constexpr (ESZ == 2)
+    if (a.H > 16 * tpr) {  // 24 columns per thread
       switch (tpr) {
         case 64: return launch_tpr<ESZ, KIND, 3, 64>(a, grid, s);
         case 128: return launch_tpr<ESZ, KIND, 3, 128>(a, grid, s);
@@ -601,24 +601,27 @@ static void launch_wide(const BwdArgs& a, bool bias, int G, hipStream_t s) {
 // while a row is summed that many keep the memory busy, and the partial rows stay a few percent of the traffic
 // (16384 x 4096 bf16 with bias: 512 workgroups 81 us, 1024 95 us, 256 128 us).  And no more than leaves each four passes
 // over its rows (2048 x 4096: 512 workgroups 18.5 us, 1024 19.8 us), but at least one per compute unit.
-static int backward_groups(int64_t T, int H, bool wide) {
-  if (wide) return (int)norm::wide_groups(T, H);
-  const int rpb = norm::rows_per_block(H);
-  const int tpr = norm::threads_per_row(H);
+static int64_t backward_groups(int64_t T, int tpr) {
+  const int rpb = tpr < 256 ? 256 / tpr : 1;
   const int64_t most = tpr <= 256 ? 512 : 256;
   const int64_t need = (T + rpb - 1) / rpb;
   if (T > 0 && need <= 4) return 1;  // a few passes of one workgroup cost less than a second launch
   int64_t g = need / 4;
   if (g < 256) g = need < 256 ? need : 256;
-  return (int)(g < most ? g : most);
+  return g < most ? g : most;
 }
 
-// Partial rows, and for wide rows the sums of every row: what the larger of the forms that rows of H columns can take needs.
+// Partial rows, and for wide rows the sums of every row: what the largest of the forms that rows of H columns can take needs.
 size_t norm_backward_floats(int64_t T, int H) {
-  const size_t held = norm::wide(H, false, false) ? 0 : 2 * (size_t)backward_groups(T, H, false) * (size_t)H;
-  const size_t wide =
-      norm::wide(H, true, true) ? 2 * (size_t)backward_groups(T, H, true) * (size_t)H + 2 * (size_t)T : 0;
-  return held > wide ? held : wide;
+  size_t most = 0;
+  for (int f32 = 0; f32 < 2; ++f32)
+    for (int bias = 0; bias < 2; ++bias) {
+      const bool wide = norm::wide(H, f32, bias);
+      const size_t G = wide ? norm::wide_groups(T, H) : backward_groups(T, norm::threads_per_row(H, f32, true));
+      const size_t floats = 2 * G * (size_t)H + (wide ? 2 * (size_t)T : 0);
+      if (floats > most) most = floats;
+    }
+  return most;
 }
 
 void launch_norm(const NormLaunch& p, hipStream_t s) {
@@ -641,7 +644,7 @@ void launch_norm(const NormLaunch& p, hipStream_t s) {
   a.mean = p.mean;
   a.rstd = p.rstd;
   const bool f32 = p.dtype == MOE_DTYPE_F32;
-  int tpr = norm::forward_threads_per_row(p.H, f32);
+  int tpr = norm::threads_per_row(p.H, f32, false);
   if (p.y_fp8 && f32 && tpr < 32) tpr = 32;  // a 128-column block of fp32 rows spans 32 lanes
   const int rpb = tpr < 256 ? 256 / tpr : 1;
   const unsigned grid = (unsigned)((p.T + rpb - 1) / rpb);
@@ -670,9 +673,10 @@ void launch_norm_backward(const NormLaunch& p, hipStream_t s) {
   a.part = p.part;
   a.dw = p.dweight;
   a.db = p.dbias;
-  const int tpr = norm::threads_per_row(p.H);
-  const bool f32 = p.dtype == MOE_DTYPE_F32, bias = p.dbias != nullptr, wide = norm::wide(p.H, f32, bias);
-  const int G = backward_groups(p.T, p.H, wide);
+  const bool f32 = p.dtype == MOE_DTYPE_F32;
+  const int tpr = norm::threads_per_row(p.H, f32, true);
+  const bool bias = p.dbias != nullptr, wide = norm::wide(p.H, f32, bias);
+  const int G = (int)(wide ? norm::wide_groups(p.T, p.H) : backward_groups(p.T, tpr));
   if (G > 0 && wide) {
     a.sums = p.part + 2 * (size_t)G * p.H;
     const bool tail = p.H % (f32 ? 4 : 8) != 0;
