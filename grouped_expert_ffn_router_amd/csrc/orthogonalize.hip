@@ -26,6 +26,7 @@
 // iteration keeps, so no product has a bound to check.  a sits on B's diagonal: X^T <- X^T (a + b A + c A A) + a lo.  A A and
 // X^T B reduce along rows of both operands; X X^T reduces over the rows of X^T, through the transposing LDS load.  Holding X
 // in both orientations instead cost an update 10 bytes per value for 6 (8 x 2048 x 7168: 615 us for 494).
+#include <type_traits>
 #include <utility>
 
 #include "common.h"
@@ -88,6 +89,8 @@ struct Args {
   int ld;
   int64_t r_batch;           // bytes between matrices
   float alpha, beta, diag;   // result = alpha * E + beta * product + diag on the diagonal (POLY)
+  _Float16* rest_of_diag;    // without SPLIT: what B's diagonal loses to its rounding, [P] per matrix (POLY writes, B X adds)
+  bool b_is_m;               // FINAL: B is the operand M
   // the first `whole` tiles are one workgroup each; `parts` workgroups share each of the rest
   int whole, parts;
   float* partial;            // [rest * parts][tile values]
@@ -353,7 +356,14 @@ struct Epilogue {
       }
       if constexpr (MODE == POLY) {
 #pragma unroll
-        for (int x = 0; x < 8; ++x) v[x] += row0 + r == col0 + c + x ? a.diag : 0.0f;
+        for (int x = 0; x < 8; ++x)
+          if (row0 + r == col0 + c + x) {
+            v[x] += a.diag;
+            if constexpr (!SPLIT) {
+              _Float16 hi;
+              split16(v[x], hi, a.rest_of_diag[(int64_t)e * a.ld + row0 + r]);
+            }
+          }
       }
       if constexpr (MODE == FINAL) {
         const int gr = row0 + r, gc = col0 + c;
@@ -478,6 +488,53 @@ __global__ __launch_bounds__((64 * Cfg<SIZE, SPLIT>::WM * Cfg<SIZE, SPLIT>::WN))
   }
 
   const int row0 = m0 + wm * WTM, col0 = n0 + wn * WTN;
+  // Without SPLIT, B's rounding to fp16 is the largest error, most of it on the diagonal, where B is of the size of a.  The
+  // 32 x 32 blocks of this wavefront's part of the diagonal get two more products each, by a fragment that is the rest of the
+  // diagonal and zero elsewhere: 1/64 more matrix instructions at P = 2048, and 1.3e-3 of the norm off instead of 2.0e-3 at
+  // 363 x 3263 (before the rounding to bf16).
+  constexpr bool DIAG = !SPLIT && (MODE == UPDATE || MODE == FINAL);
+  constexpr int DB = DIAG ? (MB > NB ? MB : NB) : 1;
+  const bool b_is_m = MODE == FINAL && a.b_is_m;
+  _Float16 rest[DB];
+  if constexpr (DIAG)
+#pragma unroll
+    for (int x = 0; x < DB; ++x) {
+      const int blocks = b_is_m ? MB : NB, first = b_is_m ? row0 : col0;
+      rest[x] = x < blocks ? a.rest_of_diag[(int64_t)e * a.m_ld + first + x * 32 + lr] : (_Float16)0.0f;
+    }
+  auto diagonal = [&](const uint8_t* As, const uint8_t* Bs, int first_k) {
+    if constexpr (DIAG) {
+#pragma unroll
+      for (int x = 0; x < DB; ++x) {
+        const int kk = (b_is_m ? row0 : col0) + x * 32 - first_k;  // of the block, in this stage
+        if (x >= (b_is_m ? MB : NB) || kk < 0 || kk >= RB / 2) continue;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          f16x8_t d;
+#pragma unroll
+          for (int y = 0; y < 8; ++y) d[y] = lr == t * 16 + lh * 8 + y ? rest[x] : (_Float16)0.0f;
+          const int s1 = RB == 128 ? t + 2 : t;
+          if (b_is_m) {
+            if (x < MB)
+#pragma unroll
+              for (int j = 0; j < NB; ++j)
+                acc[x < MB ? x : 0][j] = mfma_32x32x16(
+                    d,
+                    __builtin_bit_cast(f16x8_t, tile::lds_at(tile::to_lds(Bs) + (kk >= 32 ? bo.o[s1] : bo.o[t]),
+                                                             (brow[j] - brow[0]) * RB)),
+                    acc[x < MB ? x : 0][j]);
+          } else if (x < NB) {
+#pragma unroll
+            for (int i = 0; i < MB; ++i)
+              acc[i][x < NB ? x : 0] = mfma_32x32x16(
+                  __builtin_bit_cast(f16x8_t, tile::lds_at(tile::to_lds(As) + (kk >= 32 ? ao.o[s1] : ao.o[t]),
+                                                           (arow[i] - arow[0]) * RB)),
+                  d, acc[i][x < NB ? x : 0]);
+          }
+        }
+      }
+    }
+  };
   typename Epi::Elem el[2];
   if constexpr (SIZE == 0)
     if (parts == 1) Epi::load(a, e, row0, col0, el[0]);
@@ -486,8 +543,11 @@ __global__ __launch_bounds__((64 * Cfg<SIZE, SPLIT>::WM * Cfg<SIZE, SPLIT>::WN))
   // last iteration is then free), refills it with slice kt + NS - 1 (clamped: loaded, never read) and computes slice kt
 #pragma unroll
   for (int s = 0; s < NS - 1; ++s) load_stage(smem + s * STAGE, min(s, nk - 1));
+  if constexpr (DIAG)  // the rest of the diagonal has arrived: no stage waits for it, and so for the slices behind it
+#pragma unroll
+    for (int x = 0; x < DB; ++x) asm volatile("" : "+v"(rest[x]));
   int cb = 0, fb = NS - 1;
-  for (int kt = 0; kt < nk; ++kt) {
+  auto step = [&](int kt, auto with_diagonal) {
     wait_vmcnt<(NS - 2) * NL>();
     __syncthreads();
     load_stage(smem + fb * STAGE, min(kt + NS - 1, nk - 1));
@@ -498,8 +558,20 @@ __global__ __launch_bounds__((64 * Cfg<SIZE, SPLIT>::WM * Cfg<SIZE, SPLIT>::WN))
       mma_stage_split<RB, MB, NB>(As, As + 2 * ARR, ARR, arow, brow, ao, bo, acc);
     else
       tile::mma_stage_bf16<RB, MB, NB, f16x8_t>(As, As + ARR, arow, brow, ao, bo, acc);
+    if constexpr (decltype(with_diagonal)::value) diagonal(As, As + ARR, (k0 + kt) * (RB / 2));
     cb = cb + 1 == NS ? 0 : cb + 1;
     fb = fb + 1 == NS ? 0 : fb + 1;
+  };
+  if constexpr (DIAG) {  // three loops, so that the stages without a part of the diagonal ask nothing
+    constexpr int KS = RB / 2;
+    const int first = b_is_m ? row0 : col0, end = first + (b_is_m ? WTM : WTN);
+    const int d0 = uniform_int(max(0, min(nk, first / KS - k0))), d1 = uniform_int(max(d0, min(nk, (end + KS - 1) / KS - k0)));
+    int kt = 0;
+    for (; kt < d0; ++kt) step(kt, std::false_type{});
+    for (; kt < d1; ++kt) step(kt, std::true_type{});
+    for (; kt < nk; ++kt) step(kt, std::false_type{});
+  } else {
+    for (int kt = 0; kt < nk; ++kt) step(kt, std::false_type{});
   }
 
   // ---- a shared tile: every part leaves its sums in memory, in the accumulators' order (16 bytes per lane side by side),
@@ -579,6 +651,7 @@ __global__ __launch_bounds__(256) void narrow_kernel(const Args a, const uint8_t
   constexpr int EPI = 4 * 32 * Epi::PITCH * 4;
   constexpr int FIRST = A_ALL > EPI ? A_ALL : EPI;           // A, then the epilogue's blocks
   __shared__ __attribute__((aligned(1024))) uint8_t smem[FIRST + 2 * X_ALL];
+  __shared__ _Float16 rest[64];  // without SPLIT: what B's diagonal loses to its rounding
   uint8_t *sa = smem, *sx = smem + FIRST, *sb = sx + X_ALL;  // [stage][hi, lo][row][RB]
 
   const int lane = threadIdx.x & 63, wid = uniform_int(threadIdx.x >> 6), wm = wid >> 1, wn = wid & 1;
@@ -649,6 +722,8 @@ __global__ __launch_bounds__(256) void narrow_kernel(const Args a, const uint8_t
         v += k + x == r ? pa : 0.0f;
         _Float16 hi, lo;
         split16(v, hi, lo);
+        if constexpr (!SPLIT)
+          if (k + x == r) rest[rb] = lo;
         bh[x] = hi;
         bl[x] = lo;
       }
@@ -671,6 +746,21 @@ __global__ __launch_bounds__(256) void narrow_kernel(const Args a, const uint8_t
       mma_stage_split<RB, 1, 1>(pm, pn, X_ARR, jrow, brow, jo, bo, out);
     else
       tile::mma_stage_bf16<RB, 1, 1, f16x8_t>(pm, pn, jrow, brow, jo, bo, out);
+  }
+  if constexpr (!SPLIT) {
+    // the rest of the diagonal: rows n0 + 32 w .. of B against the same values of k, in stage n0 / 64
+    const int w = b_first ? wm : wn;
+    const _Float16 mine = rest[w * 32 + lr];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      f16x8_t d;
+#pragma unroll
+      for (int y = 0; y < 8; ++y) d[y] = lr == t * 16 + lh * 8 + y ? mine : (_Float16)0.0f;
+      const tile::FragOff& xo = b_first ? bo : jo;
+      const f16x8_t f = __builtin_bit_cast(
+          f16x8_t, tile::lds_at(tile::to_lds(sx + n0 / 64 * X_ARR) + (w == 1 ? xo.o[t + 2] : xo.o[t]), 0));
+      out[0][0] = b_first ? mfma_32x32x16(d, f, out[0][0]) : mfma_32x32x16(f, d, out[0][0]);
+    }
   }
   Epi::run(a, e, row0, col0, false, out[0], el, reinterpret_cast<float*>(sa) + wid * 32 * Epi::PITCH);
 }
@@ -855,7 +945,7 @@ struct Plan {
   int64_t chunk_values;
   Shape gram, poly, update;
   size_t x_bytes, a_bytes;  // one fp16 array of the whole batch
-  size_t part_bytes, partial, total;
+  size_t part_bytes, partial, diag_bytes, total;
 };
 
 static size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
@@ -897,7 +987,8 @@ static Plan plan_of(int64_t batch, int m, int n, bool split) {
   z.part_bytes = up256((size_t)batch * z.chunks * sizeof(double));
   for (const Shape* t : {&z.gram, &z.poly, &z.update})
     if (partial_bytes(*t) > z.partial) z.partial = partial_bytes(*t);
-  z.total = z.part_bytes + z.partial + (split ? 4 : 3) * z.x_bytes + (split ? 4 : 2) * z.a_bytes;
+  z.diag_bytes = split ? 0 : up256((size_t)batch * z.P * 2);
+  z.total = z.part_bytes + z.partial + z.diag_bytes + (split ? 4 : 3) * z.x_bytes + (split ? 4 : 2) * z.a_bytes;
   return z;
 }
 
@@ -966,6 +1057,7 @@ static void run(const OrthLaunch& p, const Plan& z, hipStream_t s) {
   };
   double* part = reinterpret_cast<double*>(take(z.part_bytes));
   float* partial = reinterpret_cast<float*>(take(z.partial));
+  _Float16* rest_of_diag = reinterpret_cast<_Float16*>(take(z.diag_bytes));
   uint8_t *y0[2] = {take(z.x_bytes), take(z.x_bytes)}, *y1[2];
   y1[0] = take(z.x_bytes);
   y1[1] = SPLIT ? take(z.x_bytes) : y1[0];  // not an operand without SPLIT: updated in place
@@ -999,6 +1091,7 @@ static void run(const OrthLaunch& p, const Plan& z, hipStream_t s) {
     const int cur = k & 1, nxt = cur ^ 1;
     Args q{};
     q.partial = partial;
+    q.rest_of_diag = rest_of_diag;
     q.M0 = q.N0 = y0[cur];  // A = X X^T
     q.M1 = q.N1 = y1[cur];
     q.m_batch = q.n_batch = xb;
@@ -1047,6 +1140,7 @@ static void run(const OrthLaunch& p, const Plan& z, hipStream_t s) {
         std::swap(q.M0, q.N0);
         std::swap(q.M1, q.N1);
         std::swap(q.m_batch, q.n_batch);
+        q.b_is_m = true;
       }
       const int rows = z.flip ? z.Q : z.P, cols = z.flip ? z.P : z.Q;
       if (z.narrow)
