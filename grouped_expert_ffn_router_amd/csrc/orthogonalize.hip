@@ -16,8 +16,8 @@
 // a^steps (485 for the usual coefficients), and with X rounded to 11 bits each step it would magnify that rounding with
 // them (a gradient of rank 1 then comes out 15% wrong, of rank 16 4%; measured in fp64 models of both).  Rounding the
 // operands of the products does not have this effect: an error in A or B multiplies X from the left, and leaves its row
-// space alone.  The last step, which magnifies by a alone, does without lo (bf16 results of 256 x 896 in the model: 2.15e-3
-// of the norm off for 2.19e-3 with lo, at rank 3 2.45e-3 for 2.24e-3; a rounding to bf16 is 1.7e-3).
+// space alone.  The last step, which magnifies by a alone, does without lo.  bf16 results of 64 x 1000 to 2048 x 7168 are 1.86
+// to 2.11e-3 of the norm off, of rank 1, 3 and 16 1.92 to 2.05e-3; their rounding alone is 1.66e-3.
 // SPLIT (fp32 outputs, and bf16 outputs of matrices so small that the launches are what is paid for) gives hi and lo to the
 // operands too and sums lo hi + hi lo + hi hi: three products, the same tiles.
 //
@@ -45,36 +45,46 @@ typedef int i32x4_e2_t __attribute__((ext_vector_type(4), aligned(2)));
 enum Mode { GRAM = 0, POLY = 1, UPDATE = 2, FINAL = 3 };
 
 // Tiles.  0: 64 x 64 over 4 wavefronts (32 x 32 each); 1: 128 x 128 over 4 (64 x 64 each); 2: 256 x 256 over 8
-// (128 x 64 each).  A stage holds RB bytes of the reduction for every tile row of each operand array (hi, and lo with
+// (128 x 64 each); 3: 256 x 192 over 8 (64 x 96 each), for X^T B where it fills the last round better (P = 1536, Q = 4096,
+// 4 matrices: 512 tiles instead of 384 on 256 compute units, 102 us instead of 117; 1 x 2304 x 4096 in all 603 instead of
+// 637), and 4, the same turned, for the last product.  A stage holds RB bytes of the reduction for every tile row of each operand array (hi, and lo with
 // SPLIT); NS stages are in flight or in use.  The small tiles' stages leave room for a second workgroup on a compute unit:
 // with SPLIT two stages of 64 x 64 instead of four took three matrices of 1001 x 333 from 186 to 163 us.
 template <int SIZE, bool SPLIT>
 struct Cfg;
 template <>
 struct Cfg<0, false> {
-  static constexpr int RB = 128, NS = 3, B = 64, WM = 2, WN = 2;
+  static constexpr int RB = 128, NS = 3, BM = 64, BN = 64, WM = 2, WN = 2;
 };
 template <>
 struct Cfg<1, false> {
-  static constexpr int RB = 64, NS = 4, B = 128, WM = 2, WN = 2;
+  static constexpr int RB = 64, NS = 4, BM = 128, BN = 128, WM = 2, WN = 2;
 };
 template <>
 struct Cfg<2, false> {
-  static constexpr int RB = 128, NS = 2, B = 256, WM = 2, WN = 4;
+  static constexpr int RB = 128, NS = 2, BM = 256, BN = 256, WM = 2, WN = 4;
 };
 template <>
 struct Cfg<0, true> {
-  static constexpr int RB = 128, NS = 2, B = 64, WM = 2, WN = 2;
+  static constexpr int RB = 128, NS = 2, BM = 64, BN = 64, WM = 2, WN = 2;
 };
 template <>
 struct Cfg<1, true> {
-  static constexpr int RB = 64, NS = 2, B = 128, WM = 2, WN = 2;
+  static constexpr int RB = 64, NS = 2, BM = 128, BN = 128, WM = 2, WN = 2;
 };
 template <>
 struct Cfg<2, true> {
-  static constexpr int RB = 64, NS = 2, B = 256, WM = 2, WN = 4;
+  static constexpr int RB = 64, NS = 2, BM = 256, BN = 256, WM = 2, WN = 4;
 };
-constexpr int TILE[3] = {64, 128, 256};
+template <>
+struct Cfg<3, false> {
+  static constexpr int RB = 128, NS = 2, BM = 256, BN = 192, WM = 4, WN = 2;
+};
+template <>
+struct Cfg<4, false> {
+  static constexpr int RB = 128, NS = 2, BM = 192, BN = 256, WM = 2, WN = 4;
+};
+constexpr int TILE_M[4] = {64, 128, 256, 256}, TILE_N[4] = {64, 128, 256, 192};
 
 struct Args {
   // operands: hi and (SPLIT) lo, fp16.  GRAM: [K][rows] per matrix of the batch (the reduction runs over rows); else [rows][K]
@@ -394,17 +404,19 @@ struct Epilogue {
 template <int MODE, int SIZE, bool SPLIT>
 __global__ __launch_bounds__((64 * Cfg<SIZE, SPLIT>::WM * Cfg<SIZE, SPLIT>::WN)) void product_kernel(const Args a) {
   using C_ = Cfg<SIZE, SPLIT>;
-  constexpr int RB = C_::RB, NS = C_::NS, B = C_::B, WM = C_::WM, WN = C_::WN, NW = WM * WN;
-  constexpr int WTM = B / WM, WTN = B / WN, MB = WTM / 32, NB = WTN / 32;
+  constexpr int RB = C_::RB, NS = C_::NS, BM = C_::BM, BN = C_::BN, WM = C_::WM, WN = C_::WN, NW = WM * WN;
+  constexpr int WTM = BM / WM, WTN = BN / WN, MB = WTM / 32, NB = WTN / 32;
   constexpr int RPI = 1024 / RB;         // rows one wavefront load instruction fills
-  constexpr int INS = B / (NW * RPI);    // load instructions per wavefront and operand array
-  constexpr int ARR = B * RB;            // bytes of an operand array in a stage
-  constexpr int NA = SPLIT ? 4 : 2;      // operand arrays
-  constexpr int STAGE = NA * ARR, NL = NA * INS, CPR = RB / 16;
-  using Epi = Epilogue<MODE, WTN, SPLIT>;
+  constexpr int INM = BM / (NW * RPI), INN = BN / (NW * RPI);  // load instructions per wavefront and operand array
+  constexpr int ARRM = BM * RB, ARRN = BN * RB;                // bytes of an operand array in a stage
+  constexpr int NA = SPLIT ? 4 : 2;                            // operand arrays, half of them M's
+  constexpr int N_AT = NA / 2 * ARRM, STAGE = N_AT + NA / 2 * ARRN, NL = NA / 2 * (INM + INN), CPR = RB / 16;
+  constexpr int EW = WTN % 64 == 0 ? WTN : 32;                 // columns that the epilogue takes at a time
+  using Epi = Epilogue<MODE, EW, SPLIT>;
   constexpr int EPI = NW * 32 * Epi::PITCH * 4;
   constexpr int SMEM = NS * STAGE > EPI ? NS * STAGE : EPI;
   constexpr bool SYM = Epi::SYM, TR = MODE == GRAM;
+  static_assert(BM == BN || (!SYM && !SPLIT), "rectangular tiles: X B only");
   __shared__ __attribute__((aligned(1024))) uint8_t smem[SMEM];
 
   const int lane = threadIdx.x & 63, wid = uniform_int(threadIdx.x >> 6);
@@ -421,7 +433,7 @@ __global__ __launch_bounds__((64 * Cfg<SIZE, SPLIT>::WM * Cfg<SIZE, SPLIT>::WN))
     L = a.whole + (L - a.whole) / parts;
   }
   const TileAt at = tile_at<MODE>(a, L);
-  const int e = at.e, m0 = at.mi * B, n0 = at.ni * B;
+  const int e = at.e, m0 = at.mi * BM, n0 = at.ni * BN;
   // this workgroup's stages, and a stage's step in memory (bytes)
   const int nk_all = a.K * 2 / RB;
   const int k0 = uniform_int((int)((int64_t)nk_all * part / parts));
@@ -437,29 +449,36 @@ __global__ __launch_bounds__((64 * Cfg<SIZE, SPLIT>::WM * Cfg<SIZE, SPLIT>::WN))
     base[1] = uniform_ptr(a.M1 + moff);
     base[3] = uniform_ptr(a.N1 + noff);
   }
-  uint32_t m_off[INS], n_off[INS];
-#pragma unroll
-  for (int q = 0; q < INS; ++q) {
-    int r, at;  // row, and byte in it, of this lane's 16 bytes
+  uint32_t m_off[INM], n_off[INN];
+  auto offset = [&](int instr, int64_t row_bytes) {  // of this lane's 16 bytes of an operand array
+    int r, at;                                       // row, and byte in it
     if constexpr (TR) {
-      constexpr int PIECES = B / 8;
-      r = (wid * INS + q) * (64 / PIECES) + lane / PIECES;
+      constexpr int PIECES = BM / 8;
+      r = instr * (64 / PIECES) + lane / PIECES;
       const int piece = lane % PIECES;
-      at = (((piece / 4) ^ swz_t<B>(r)) * 4 + piece % 4) * 16;
+      at = (((piece / 4) ^ swz_t<BM>(r)) * 4 + piece % 4) * 16;
     } else {
-      r = (wid * INS + q) * RPI + lane / CPR;
+      r = instr * RPI + lane / CPR;
       at = ((lane % CPR) ^ tile::swz<RB>(r)) * 16;
     }
-    m_off[q] = (uint32_t)(r * m_row + at);
-    n_off[q] = (uint32_t)(r * n_row + at);
-  }
+    return (uint32_t)(r * row_bytes + at);
+  };
+#pragma unroll
+  for (int q = 0; q < INM; ++q) m_off[q] = offset(wid * INM + q, m_row);
+#pragma unroll
+  for (int q = 0; q < INN; ++q) n_off[q] = offset(wid * INN + q, n_row);
   auto load_stage = [&](uint8_t* dst, int kt) {
 #pragma unroll
-    for (int x = 0; x < NA; ++x) {
-      const uint8_t* p = uniform_ptr(base[x] + kt * (x < NA / 2 ? m_step : n_step));
+    for (int x = 0; x < NA / 2; ++x) {
+      const uint8_t* p = uniform_ptr(base[x] + kt * m_step);
 #pragma unroll
-      for (int q = 0; q < INS; ++q)
-        load_lds16(p, x < NA / 2 ? m_off[q] : n_off[q], dst + x * ARR + (wid * INS + q) * 1024);
+      for (int q = 0; q < INM; ++q) load_lds16(p, m_off[q], dst + x * ARRM + (wid * INM + q) * 1024);
+    }
+#pragma unroll
+    for (int x = 0; x < NA / 2; ++x) {
+      const uint8_t* p = uniform_ptr(base[NA / 2 + x] + kt * n_step);
+#pragma unroll
+      for (int q = 0; q < INN; ++q) load_lds16(p, n_off[q], dst + N_AT + x * ARRN + (wid * INN + q) * 1024);
     }
   };
 
@@ -482,19 +501,19 @@ __global__ __launch_bounds__((64 * Cfg<SIZE, SPLIT>::WM * Cfg<SIZE, SPLIT>::WN))
   {
     const int k = (lane >> 5) * 8 + (lane >> 2 & 3), in = (lane >> 4 & 1) * 32 + (lane & 3) * 8;
 #pragma unroll
-    for (int i = 0; i < MB; ++i) at_m[i] = (uint32_t)(k * 2 * B + ((wm * MB + i) ^ swz_t<B>(k)) * 64 + in);
+    for (int i = 0; i < MB; ++i) at_m[i] = (uint32_t)(k * 2 * BM + ((wm * MB + i) ^ swz_t<BM>(k)) * 64 + in);
 #pragma unroll
-    for (int j = 0; j < NB; ++j) at_n[j] = (uint32_t)(k * 2 * B + ((wn * NB + j) ^ swz_t<B>(k)) * 64 + in);
+    for (int j = 0; j < NB; ++j) at_n[j] = (uint32_t)(k * 2 * BM + ((wn * NB + j) ^ swz_t<BM>(k)) * 64 + in);
   }
 
   const int row0 = m0 + wm * WTM, col0 = n0 + wn * WTN;
   // Without SPLIT, B's rounding to fp16 is the largest error, most of it on the diagonal, where B is of the size of a.  The
   // 32 x 32 blocks of this wavefront's part of the diagonal get two more products each, by a fragment that is the rest of the
-  // diagonal and zero elsewhere: 1/64 more matrix instructions at P = 2048, and 1.3e-3 of the norm off instead of 2.0e-3 at
-  // 363 x 3263 (before the rounding to bf16).
+  // diagonal and zero elsewhere: 1/64 more matrix instructions at P = 2048 (16 more us of 4500 for 8 x 2048 x 7168), and
+  // 2.11e-3 of the norm off instead of 2.7e-3 at 363 x 3263.
   constexpr bool DIAG = !SPLIT && (MODE == UPDATE || MODE == FINAL);
   constexpr int DB = DIAG ? (MB > NB ? MB : NB) : 1;
-  const bool b_is_m = MODE == FINAL && a.b_is_m;
+  const bool b_is_m = SIZE == 4 || (SIZE < 3 && MODE == FINAL && a.b_is_m);
   _Float16 rest[DB];
   if constexpr (DIAG)
 #pragma unroll
@@ -553,12 +572,12 @@ __global__ __launch_bounds__((64 * Cfg<SIZE, SPLIT>::WM * Cfg<SIZE, SPLIT>::WN))
     load_stage(smem + fb * STAGE, min(kt + NS - 1, nk - 1));
     const uint8_t* As = smem + cb * STAGE;
     if constexpr (TR)
-      mma_stage_t<RB, B, SPLIT, MB, NB>(As, As + NA / 2 * ARR, at_m, at_n, acc);
+      mma_stage_t<RB, BM, SPLIT, MB, NB>(As, As + N_AT, at_m, at_n, acc);
     else if constexpr (SPLIT)
-      mma_stage_split<RB, MB, NB>(As, As + 2 * ARR, ARR, arow, brow, ao, bo, acc);
+      mma_stage_split<RB, MB, NB>(As, As + N_AT, ARRM, arow, brow, ao, bo, acc);
     else
-      tile::mma_stage_bf16<RB, MB, NB, f16x8_t>(As, As + ARR, arow, brow, ao, bo, acc);
-    if constexpr (decltype(with_diagonal)::value) diagonal(As, As + ARR, (k0 + kt) * (RB / 2));
+      tile::mma_stage_bf16<RB, MB, NB, f16x8_t>(As, As + N_AT, arow, brow, ao, bo, acc);
+    if constexpr (decltype(with_diagonal)::value) diagonal(As, As + N_AT, (k0 + kt) * (RB / 2));
     cb = cb + 1 == NS ? 0 : cb + 1;
     fb = fb + 1 == NS ? 0 : fb + 1;
   };
@@ -577,7 +596,7 @@ __global__ __launch_bounds__((64 * Cfg<SIZE, SPLIT>::WM * Cfg<SIZE, SPLIT>::WN))
   // ---- a shared tile: every part leaves its sums in memory, in the accumulators' order (16 bytes per lane side by side),
   // for the launch that joins them
   if (parts > 1) {
-    float* mine = a.partial + ((int64_t)(L - a.whole) * parts + part) * (B * B) + wid * (WTM * WTN) + lane * 4;
+    float* mine = a.partial + ((int64_t)(L - a.whole) * parts + part) * (BM * BN) + wid * (WTM * WTN) + lane * 4;
 #pragma unroll
     for (int i = 0; i < MB; ++i)
 #pragma unroll
@@ -597,10 +616,15 @@ __global__ __launch_bounds__((64 * Cfg<SIZE, SPLIT>::WM * Cfg<SIZE, SPLIT>::WN))
   wait_vmcnt0();
   __syncthreads();  // no load into LDS in flight, no wavefront still reading a stage: the epilogue reuses the buffers
   float* sc = reinterpret_cast<float*>(smem) + wid * 32 * Epi::PITCH;
+  constexpr int PIECES = WTN / EW;
 #pragma unroll
-  for (int i = 0; i < MB; ++i) {
-    if (i + 1 < MB) Epi::load(a, at.e, row0 + (i + 1) * 32, col0, el[(i + 1) & 1]);
-    Epi::run(a, at.e, row0 + i * 32, col0, mirror, acc[i], el[i & 1], sc);
+  for (int u = 0; u < MB * PIECES; ++u) {
+    const int i = u / PIECES, c = u % PIECES * EW, next = (u + 1) / PIECES;
+    if (next < MB) Epi::load(a, at.e, row0 + next * 32, col0 + (u + 1) % PIECES * EW, el[(u + 1) & 1]);
+    f32x16_t block[Epi::NB];
+#pragma unroll
+    for (int x = 0; x < Epi::NB; ++x) block[x] = acc[i][c / 32 + x];
+    Epi::run(a, at.e, row0 + i * 32, col0 + c, mirror, block, el[u & 1], sc);
   }
 }
 
@@ -608,7 +632,7 @@ __global__ __launch_bounds__((64 * Cfg<SIZE, SPLIT>::WM * Cfg<SIZE, SPLIT>::WN))
 template <int MODE, int SIZE, bool SPLIT>
 __global__ __launch_bounds__(256) void join_kernel(const Args a) {
   using C_ = Cfg<SIZE, SPLIT>;
-  constexpr int B = C_::B, WTM = B / C_::WM, WTN = B / C_::WN, MB = WTM / 32, NB = WTN / 32;
+  constexpr int B = C_::BM, WTM = B / C_::WM, WTN = B / C_::WN, MB = WTM / 32, NB = WTN / 32;
   constexpr int BLOCKS = C_::WM * C_::WN * MB;  // of a tile
   using Epi = Epilogue<MODE, WTN, SPLIT>;
   __shared__ float smem[4 * 32 * Epi::PITCH];
@@ -898,18 +922,19 @@ struct Shape {
 // Microseconds of a product, to choose by: a launch of its own, then for every 256 tiles (one per compute unit; two smaller
 // tiles that share one take as long as one after the other) the reduction and the epilogue.  Measured on kernels of 24 to
 // 8192 tiles, K = 512 to 14336; one 256 x 256 tile holds 16 of 64 x 64, so per value the sizes cost 22 : 37 : 67.
-//                               64 x 64        128 x 128      256 x 256
-constexpr double PER_K[2][3] = {{4.2e-3, 9.2e-3, 22e-3}, {8.5e-3, 27e-3, 72e-3}};  // [SPLIT]
+// Columns: 64 x 64, 128 x 128, 256 x 256, 256 x 192.
+constexpr double PER_K[2][4] = {{4.2e-3, 9.2e-3, 22e-3, 17.5e-3}, {8.5e-3, 27e-3, 72e-3}};  // [SPLIT]
 constexpr double EPI_SYM[2][3] = {{1.0, 4.0, 10.0}, {1.5, 6.0, 15.0}};
-constexpr double EPI_UPDATE[2][3] = {{1.0, 5.0, 19.0}, {1.5, 7.0, 28.0}};
+constexpr double EPI_UPDATE[2][4] = {{1.0, 5.0, 19.0, 14.5}, {1.5, 7.0, 28.0}};
 constexpr double LAUNCH_US = 4.5, BYTES_PER_US = 4e6;
 
-static Shape shape(int64_t batch, int rows, int cols, int K, bool sym, int most_size, bool split) {
+static Shape shape(int64_t batch, int rows, int cols, int K, bool sym, bool split) {
   Shape best{};
   best.us = 1e30;
-  for (int size = 0; size <= most_size; ++size) {
-    const int64_t nt = cols / TILE[size];
-    const int64_t tiles = (sym ? nt * (nt + 1) / 2 : (int64_t)(rows / TILE[size]) * nt) * batch;
+  for (int size = 0; size < (sym || split ? 3 : 4); ++size) {
+    const int tm = TILE_M[size], tn = TILE_N[size];
+    if (rows % tm != 0 || cols % tn != 0) continue;
+    const int64_t nt = cols / tn, tiles = (sym ? nt * (nt + 1) / 2 : (int64_t)(rows / tm) * nt) * batch;
     const double epi = sym ? EPI_SYM[split][size] : EPI_UPDATE[split][size], red = K * PER_K[split][size];
     const int64_t full = tiles / CUS;
     const int rest = (int)(tiles % CUS);
@@ -918,8 +943,9 @@ static Shape shape(int64_t batch, int rows, int cols, int K, bool sym, int most_
     int parts = rest > 0 ? CUS / rest : 1;
     if (parts > MOST_PARTS) parts = MOST_PARTS;
     if (parts > stages / 4) parts = stages / 4;
+    if (size == 3) parts = 1;  // chosen where it fills its last round: nothing to share
     for (int x = 1; x <= (parts < 1 ? 1 : parts); ++x) {
-      const double bytes = 2.0 * rest * x * TILE[size] * TILE[size] * sizeof(float);
+      const double bytes = 2.0 * rest * x * tm * tn * sizeof(float);
       const double us = LAUNCH_US + full * (red + epi) +
                         (rest == 0 ? 0.0 : x == 1 ? red + epi : red / x + LAUNCH_US + bytes / BYTES_PER_US);
       if (us < best.us) {
@@ -934,7 +960,7 @@ static Shape shape(int64_t batch, int rows, int cols, int K, bool sym, int most_
   return best;
 }
 static size_t partial_bytes(const Shape& z) {
-  return (size_t)z.rest * z.parts * TILE[z.size] * TILE[z.size] * sizeof(float);
+  return (size_t)z.rest * z.parts * TILE_M[z.size] * TILE_N[z.size] * sizeof(float);
 }
 
 struct Plan {
@@ -956,12 +982,12 @@ static Plan plan_of(int64_t batch, int m, int n, bool split) {
   z.flip = m > n;
   z.p = z.flip ? n : m;
   z.q = z.flip ? m : n;
-  // the largest tile that the products choose from sets the padding: the least sum of the estimates
+  // padding to multiples of the tile sizes (384: of 128 and 192): the least sum of the estimates
   z.us = 1e30;
-  for (int most = 0; most < 3; ++most) {
-    const int tl = TILE[most], P = (z.p + tl - 1) / tl * tl, Q = (z.q + tl - 1) / tl * tl;
-    const Shape gram = shape(batch, P, P, Q, true, most, split), poly = shape(batch, P, P, P, true, most, split),
-                update = shape(batch, Q, P, P, false, most, split);
+  for (const auto [to_p, to_q] : {std::pair{64, 64}, {128, 128}, {256, 256}, {384, 256}}) {
+    const int P = (z.p + to_p - 1) / to_p * to_p, Q = (z.q + to_q - 1) / to_q * to_q;
+    const Shape gram = shape(batch, P, P, Q, true, split), poly = shape(batch, P, P, P, true, split),
+                update = shape(batch, Q, P, P, false, split);
     if (gram.us + poly.us + update.us < z.us) {
       z.us = gram.us + poly.us + update.us;
       z.P = P;
@@ -993,8 +1019,7 @@ static Plan plan_of(int64_t batch, int m, int n, bool split) {
 }
 
 // bf16 results take the split form where the estimates are close: it brings them to their own rounding (1.7e-3 of the norm
-// off; a side of 64 and less is 2.5 to 2.9e-3 off without it, of 2048 2.0e-3), and a 64 x 64 takes 67 us either way, where
-// 4 x 100 x 1000 takes 91 us instead of 71.
+// off; 1.9 to 2.1e-3 without it), and a 64 x 64 takes 67 us either way, where 4 x 100 x 1000 takes 91 us instead of 71.
 static Plan plan(int64_t batch, int m, int n, bool out_bf16) {
   const Plan split = plan_of(batch, m, n, true);
   if (!out_bf16) return split;
@@ -1007,19 +1032,26 @@ static void launch_sized(const Args& a, const Shape& z, hipStream_t s) {
   using C_ = Cfg<SIZE, SPLIT>;
   hipLaunchKernelGGL((product_kernel<MODE, SIZE, SPLIT>), dim3((unsigned)(z.whole + z.rest * z.parts)),
                      dim3(64 * C_::WM * C_::WN), 0, s, a);
-  // 32-row blocks of a tile: SIZE 0: 2 x 2 x 1, 1: 2 x 2 x 2, 2: 2 x 4 x 4; four to a workgroup
-  constexpr int GROUPS = C_::WM * C_::WN * (C_::B / C_::WM / 32) / 4;
-  if (z.rest > 0)
-    hipLaunchKernelGGL((join_kernel<MODE, SIZE, SPLIT>), dim3((unsigned)(z.rest * GROUPS)), dim3(256), 0, s, a);
+  // 32-row blocks of a tile, joined by a launch of their own: SIZE 0: 2 x 2 x 1, 1: 2 x 2 x 2, 2: 2 x 4 x 4; four to a workgroup
+  constexpr int GROUPS = C_::WM * C_::WN * (C_::BM / C_::WM / 32) / 4;
+  if constexpr (SIZE < 3)
+    if (z.rest > 0)
+      hipLaunchKernelGGL((join_kernel<MODE, SIZE, SPLIT>), dim3((unsigned)(z.rest * GROUPS)), dim3(256), 0, s, a);
 }
 
 template <int MODE, bool SPLIT>
 static void launch_product(const Args& a0, const Shape& z, int rows, int cols, hipStream_t s) {
   Args a = a0;
-  a.mt = rows / TILE[z.size];
-  a.nt = cols / TILE[z.size];
+  a.mt = rows / (a.b_is_m ? TILE_N : TILE_M)[z.size];
+  a.nt = cols / (a.b_is_m ? TILE_M : TILE_N)[z.size];
   a.whole = z.whole;
   a.parts = z.parts;
+  if constexpr (!SPLIT && (MODE == UPDATE || MODE == FINAL))
+    if (z.size == 3) {
+      if constexpr (MODE == FINAL)
+        if (a.b_is_m) return launch_sized<FINAL, 4, false>(a, z, s);
+      return launch_sized<MODE, 3, false>(a, z, s);
+    }
   if (z.size == 2)
     launch_sized<MODE, 2, SPLIT>(a, z, s);
   else if (z.size == 1)

@@ -418,8 +418,8 @@ moe_status moe_norm_backward(const void* dy, int64_t ld_dy, const void* s, int64
  *        with an infinity or a NaN gives NaN, and touches no other matrix of the batch.
  *   out  (device) [batch, m, n] out, out_dtype F32 or BF16; must not overlap g.
  * Precision: products of fp16 operands accumulated in fp32, X kept to 22 bits between the steps.  out_dtype BF16 takes
- * each operand to one fp16 value: with the rounding to bf16 |error|_F is 2.0 to 2.3e-3 |out|_F (the rounding alone is
- * 1.7e-3; up to 2.8e-3 at rank 1).  F32 takes each operand to two (hi + lo, 22 bits) and three products: fp32's accuracy at
+ * each operand to one fp16 value (a's place on the diagonal to two): with the rounding to bf16 |error|_F is 1.9 to 2.1e-3
+ * |out|_F, at low ranks too (the rounding alone is 1.7e-3).  F32 takes each operand to two (hi + lo, 22 bits) and three products: fp32's accuracy at
  * three times the products' cost; so does BF16 where a batch is so small that this costs nothing.
  *   X's values are held to 2^-37 at least: a g whose norm is below about 1e-9 eps gives zeros.
  *   workspace (device) at least moe_orthogonalize_workspace_bytes(batch, m, n, out_dtype) bytes, 256-byte aligned; calls

@@ -81,6 +81,32 @@ def test_large_tiles(B, mm, n, out_dtype):
     check(out, definition(g))
 
 
+# sides and batches for which tiles of 256 x 192 leave the least of a last round empty
+@pytest.mark.parametrize("B,mm,n", [(4, 768, 4090), (4, 4090, 768), (1, 2301, 4000), (2, 1500, 4096)])
+def test_rectangular_tiles(B, mm, n):
+    g = normal(2, B, mm, n) * 0.02
+    check(m.moe_orthogonalize(g, out_dtype=torch.bfloat16), definition(g))
+
+
+# One step with b = c = 0 gives a X_0.  a = 1 + 2^-11 is halfway between two fp16 values: with B rounded to fp16 alone every
+# value comes out 2^-11 too small.  The errors' mean along the result shows it, for what single roundings add to it is small:
+# 0.41 * 2^-8 of a value each over N normal values is sqrt(3 / N) 0.41 2^-8, 1.2e-5 at N = 60 000; five of these are 2^-14.
+# The last product's X is the fp16 hi part, though, and 11 bits rounded to bf16's 8 are not even: a value m 2^e (1 <= m < 2)
+# lies at k / 8 of a bf16 step (2^-7 2^e), k = 0 .. 7 equally likely, and a moves it on by f / 8, f = m / 2.  Those with
+# k >= 4 round up, the others down: (4 - 8 f) / 64 of a step on average, (1 - m) / 16, which is (m - 1) / m 2^-11 of the value
+# and at most 2^-12.  So 2^-12 + 2^-14 (3.1e-4) is allowed, and a rounded a is 4.9e-4 off.
+@pytest.mark.parametrize("B,mm,n", [(16, 60, 1000), (64, 1000, 60), (64, 128, 500), (40, 1000, 100), (33, 192, 1100),
+                                    (20, 1100, 192), (6, 512, 2048), (6, 2000, 512), (4, 768, 4090), (4, 4090, 768),
+                                    (4, 2048, 2048), (1, 363, 3263)])
+def test_a_is_not_rounded_with_the_diagonal(B, mm, n):
+    a = 1 + 2.0**-11
+    g = normal(8, B, mm, n)
+    got = m.moe_orthogonalize(g, steps=1, coeffs=(a, 0.0, 0.0), out_dtype=torch.bfloat16).double()
+    for e, x in zip(got, g.double()):
+        w = a * x / (x.norm() + 1e-7)
+        assert abs(float(((e - w) * w).sum() / (w * w).sum())) <= 2.0**-12 + 2.0**-14
+
+
 @pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("rank", [1, 3, 40])
 def test_low_rank(rank, out_dtype):
