@@ -7,10 +7,11 @@
 //
 // Bound by memory: forward reads x (and residual) and writes y (and s) once, backward reads dy and s (and dsum) and
 // writes ds once; a row stays in registers between its statistics and its result.  TPR threads share a row, 16
-// columns each (TPR = 16 .. 1024 by powers of two; forward bf16 rows 24 where fewer threads then idle, above 16384 columns
-// 64, wide backward ones a form of their own), so a thread has two to four 16-byte loads of each operand in flight and the two sums of a row cost one or two exchanges: in a wavefront
-// by lane shuffles, across wavefronts through LDS.  Rows of any width, stride and alignment take the same 16-byte
-// accesses, at the element's alignment; only a row's last few elements go one by one.
+// columns each (TPR = 16 .. 1024 by powers of two; bf16 rows 24 where fewer threads then idle; above 16384 columns forward ones
+// 64, and wide backward ones take a form of their own), so a thread has two to four 16-byte loads of each operand in flight
+// and the two sums of a row cost one or two exchanges: in a wavefront by lane shuffles, across wavefronts through LDS.
+// Rows of any width, stride and alignment take the same 16-byte accesses, at the element's alignment; only a row's last
+// few elements go one by one.
 // Statistics: the mean first, then the squares of the differences, both in fp32 from registers: no cancellation of
 // E[s^2] - m^2.
 //
@@ -252,7 +253,7 @@ __global__ __launch_bounds__((TPR < 256 ? 256 : TPR)) void norm_fwd_kernel(const
       for (int e = 0; e < VEC; ++e) amax = fmaxf(amax, c < a.H ? fabsf(y[e]) : 0.0f);
 #pragma unroll
       for (int o = 64 / VEC; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor(amax, o, 64));
-      const float sc = amax > 0.0f ? amax / 448.0f : 1.0f;
+      const float q448 = amax / 448.0f, sc = q448 > 0.0f ? q448 : 1.0f;  // 0 too where amax is below 448 * 2^-150
       if (c < a.H && live) {
         uint32_t code[VEC / 4];
 #pragma unroll
@@ -647,11 +648,25 @@ void launch_norm(const NormLaunch& p, hipStream_t s) {
   int tpr = norm::threads_per_row(p.H, f32, false);
   if (p.y_fp8 && f32 && tpr < 32) tpr = 32;  // a 128-column block of fp32 rows spans 32 lanes
   const int rpb = tpr < 256 ? 256 / tpr : 1;
-  const unsigned grid = (unsigned)((p.T + rpb - 1) / rpb);
-  if (f32)
-    norm::launch_shape<4, norm::FWD>(a, tpr, grid, s);
-  else
-    norm::launch_shape<2, norm::FWD>(a, tpr, grid, s);
+  const int64_t most = (1ll << 31) / (tpr < 256 ? 256 : tpr) * rpb;  // rows of a launch: a grid has less than 2^32 threads
+  const size_t es = f32 ? 4 : 2;
+  for (int64_t left = p.T; left > 0; left -= a.T) {
+    a.T = left < most ? left : most;
+    const unsigned grid = (unsigned)((a.T + rpb - 1) / rpb);
+    if (f32)
+      norm::launch_shape<4, norm::FWD>(a, tpr, grid, s);
+    else
+      norm::launch_shape<2, norm::FWD>(a, tpr, grid, s);
+    a.x += a.T * a.ldx * es;
+    if (a.res != nullptr) {
+      a.res += a.T * a.ldr * es;
+      a.sum += a.T * a.H * es;
+    }
+    a.y += a.T * a.H * (a.y_fp8 ? 1 : es);
+    if (a.y_fp8) a.ys += a.T * (a.H / 128);
+    if (a.mean != nullptr) a.mean += a.T;
+    if (a.rstd != nullptr) a.rstd += a.T;
+  }
 }
 
 void launch_norm_backward(const NormLaunch& p, hipStream_t s) {

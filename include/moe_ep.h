@@ -376,7 +376,7 @@ moe_status moe_grouped_ffn_backward(const void* dout, int64_t T, int32_t k, int3
  *            residual itself (contiguous rows); outputs overlap no input otherwise.
  *   y        (device) [T, H] contiguous out, y_dtype: dtype, or FP8_E4M3 with y_scales (device) [T, H/128] fp32 out,
  *            the form moe_dispatch_permute takes: per row and 128 columns scale = amax / 448 (amax over the values
- *            that are not NaN; 1 where amax is 0), code = y / scale rounded to nearest even, NaN kept.  FP8_E4M3
+ *            that are not NaN; 1 where amax / 448 is 0), code = y / scale rounded to nearest even, NaN kept.  FP8_E4M3
  *            needs H % 128 == 0 and a 16-byte aligned y.  y_scales is unused otherwise.
  *   mean, rstd (device) [T] fp32 out, each may be NULL; mean is not written for MOE_NORM_RMS.
  * Alignment: the element size.

@@ -340,3 +340,30 @@ def test_other_stream_and_two_calls():
         assert all(torch.equal(a[k], c[k]) for k in a)
     with pytest.raises(ValueError):
         m.moe_norm(x, w, stream=streams[0].cuda_stream)  # a raw handle: the caller passes every buffer
+
+
+def test_e4m3_of_values_that_have_no_scale():
+    """A block whose largest value / 448 is 0 in fp32 (below 448 * 2^-150) has scale 1, and codes of 0."""
+    x = normal(31, 3, 256).bfloat16()
+    w = torch.zeros(256, device="cuda")
+    w[5], w[200] = 1e-43, 1.0
+    r = m.moe_norm(x, w, kind="rms", out_dtype=torch.float8_e4m3fn)
+    assert torch.equal(r.y_scales[:, 0], torch.ones(3, device="cuda"))
+    assert (r.y.view(torch.uint8)[:, :128] & 0x7F == 0).all()
+    assert (r.y.float()[:, 200].abs() == 448).all()
+
+
+@pytest.mark.parametrize("H,residual", [(1, False), (3, True)])
+def test_more_rows_than_one_grid_holds(H, residual):
+    """16 threads a row, 2^28 rows and more: 2^32 threads.  Rows around the places where a grid may end, and the last ones."""
+    T = (1 << 28) + 37
+    x = torch.arange(T * H, device="cuda", dtype=torch.int32).remainder_(251).to(torch.bfloat16).view(T, H)
+    w = torch.tensor([1.0, -2.0, 0.5], device="cuda")[:H].contiguous()
+    b = None if residual else w + 1
+    r = m.moe_norm(x, w, b, residual=x if residual else None, kind="rms", eps=1.0)
+    for lo in (0, (1 << 27) - 20, (1 << 28) - 20, T - 40):
+        rows = x[lo:lo + 40]
+        want = m.moe_norm(rows, w, b, residual=rows if residual else None, kind="rms", eps=1.0)
+        assert torch.equal(r.y[lo:lo + 40], want.y) and torch.equal(r.rstd[lo:lo + 40], want.rstd)
+        if residual:
+            assert torch.equal(r.sum[lo:lo + 40], want.sum)
