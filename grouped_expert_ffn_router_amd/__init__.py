@@ -770,7 +770,8 @@ class MoELayer:
                                        dbias=None if norm_bias is None
                                        else torch.empty(H, dtype=torch.float32, device=d))
                 self.ws_norm = torch.empty(moe_norm_backward_workspace_bytes(T, H), dtype=torch.uint8, device=d)
-        self.updates = self.ws_orth = None
+        self.updates = None
+        self.orth_buffers = {}  # by type, so that a captured call keeps its own
 
     def _need(self, what, ok):
         if not ok:
@@ -798,20 +799,20 @@ class MoELayer:
     def orthogonalize(self, steps=5, coeffs=ORTHOGONALIZE_COEFFS, eps=1e-7, scale=1.0, out_dtype=torch.bfloat16,
                       stream=None):
         """Orthogonalised updates of the last backward()'s weight gradients, one matrix per local expert: dict(w_gate,
-        w_up, w_down) of tensors that the layer keeps (as their workspace) from the first call on."""
+        w_up, w_down) of tensors that the layer keeps (as their workspace) from the first call with out_dtype on."""
         self._need("orthogonalize() needs a layer built with train=True", self.train)
         El, H, F = self.w_nat[0].shape
-        if self.updates is None or self.updates["w_gate"].dtype != out_dtype:
+        if out_dtype not in self.orth_buffers:
             with _alloc_on(stream):
                 d = self.grads["dx"].device
-                self.updates = {k: torch.empty(self.grads["d" + k].shape, dtype=out_dtype, device=d)
-                                for k in ("w_gate", "w_up", "w_down")}
-                self.ws_orth = torch.empty(max(moe_orthogonalize_workspace_bytes(El, H, F, out_dtype),
-                                               moe_orthogonalize_workspace_bytes(El, F, H, out_dtype)),
-                                           dtype=torch.uint8, device=d)
+                ws = torch.empty(max(moe_orthogonalize_workspace_bytes(El, H, F, out_dtype),
+                                     moe_orthogonalize_workspace_bytes(El, F, H, out_dtype)),
+                                 dtype=torch.uint8, device=d)
+                self.orth_buffers[out_dtype] = {k: torch.empty(self.grads["d" + k].shape, dtype=out_dtype, device=d)
+                                                for k in ("w_gate", "w_up", "w_down")}, ws
+        self.updates, ws = self.orth_buffers[out_dtype]
         for k, u in self.updates.items():
-            moe_orthogonalize(self.grads["d" + k], steps, coeffs, eps, scale, out=u, workspace=self.ws_orth,
-                              stream=stream)
+            moe_orthogonalize(self.grads["d" + k], steps, coeffs, eps, scale, out=u, workspace=ws, stream=stream)
         return self.updates
 
     def forward_train(self, stream=None):

@@ -791,13 +791,11 @@ moe_status moe_orthogonalize(const void* g, moe_dtype g_dtype, int64_t batch, in
   if (!iteration_bounded(steps, a, b, c))
     FAIL(MOE_ERR_INVALID_ARG, "%s: the coefficients (%g, %g, %g) do not keep %d steps bounded", fn, (double)a, (double)b,
          (double)c, steps);
-  // tiles of 128 x 128 over the whole batch are one grid
-  const int64_t tiles = ((m + 255) / 256 * 2) * (int64_t)((n + 255) / 256 * 2);
-  if (tiles * batch >= (1ll << 28)) FAIL(MOE_ERR_INVALID_ARG, "%s: batch * m * n is too large for one launch", fn);
   if (batch == 0) return MOE_OK;
   REQ_PTR(g, dtype_bytes(g_dtype), "g");
   REQ_PTR(out, dtype_bytes(out_dtype), "out");
   const size_t need = moe_orthogonalize_workspace_bytes(batch, m, n, out_dtype);
+  if (need == 0) FAIL(MOE_ERR_INVALID_ARG, "%s: batch * m * n is too large for one launch", fn);
   if (workspace == nullptr || workspace_bytes < need || !aligned(workspace, 256))
     FAIL(MOE_ERR_WORKSPACE, "%s: workspace needs %zu bytes, 256-byte aligned (got %zu)", fn, need, workspace_bytes);
   OrthLaunch p{};

@@ -113,7 +113,7 @@ struct OrthLaunch {
   bool out_bf16;
   void* workspace;
 };
-size_t orthogonalize_workspace(int64_t batch, int m, int n, bool out_bf16);
+size_t orthogonalize_workspace(int64_t batch, int m, int n, bool out_bf16);  // 0: too large for one launch
 void launch_orthogonalize(const OrthLaunch& p, hipStream_t s);
 
 }  // namespace moe

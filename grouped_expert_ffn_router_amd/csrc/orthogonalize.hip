@@ -1186,7 +1186,9 @@ static void run(const OrthLaunch& p, const Plan& z, hipStream_t s) {
 }  // namespace orth
 
 size_t orthogonalize_workspace(int64_t batch, int m, int n, bool out_bf16) {
-  return orth::plan(batch, m, n, out_bf16).total;
+  const orth::Plan z = orth::plan(batch, m, n, out_bf16);
+  // the largest grid has a workgroup of 256 per 64 x 64 values, and a grid less than 2^32 threads
+  return batch * (z.P / 64) * (z.Q / 64) < (1 << 24) ? z.total : 0;
 }
 
 void launch_orthogonalize(const OrthLaunch& p, hipStream_t s) {

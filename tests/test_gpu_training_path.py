@@ -89,6 +89,19 @@ def test_gradients_of_a_step():
         check_orthogonal(up[name], definition(g["d" + name]), low_rank=True)
 
 
+def test_updates_of_another_type_leave_a_captured_call_alone():
+    layer, _, x, res, wr, rnd = build("f32", "layer", True)
+    for g in layer.grads.values():
+        g.copy_(torch.randn_like(g))
+    first = layer.orthogonalize(out_dtype=torch.bfloat16)
+    pointers = {k: u.data_ptr() for k, u in first.items()}
+    other = layer.orthogonalize(out_dtype=torch.float32)
+    again = layer.orthogonalize(out_dtype=torch.bfloat16)
+    assert {k: u.data_ptr() for k, u in again.items()} == pointers
+    assert not set(pointers.values()) & {u.data_ptr() for u in other.values()}
+    assert other["w_gate"].dtype == torch.float32 and layer.updates is again
+
+
 def test_step_in_one_graph():
     layer, _, x, res, wr, rnd = build("bf16", "rms", True, T=512, H=512, E=4, F=512)
     dout = rnd(512, 512).bfloat16()

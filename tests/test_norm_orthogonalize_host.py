@@ -85,6 +85,7 @@ def test_norm_backward_workspace():
     (dict(n=65537), "n ="), (dict(steps=0), "steps"), (dict(steps=33), "steps"), (dict(eps=0.0), "eps"),
     (dict(eps=float("nan")), "eps"), (dict(eps=float("inf")), "eps"), (dict(scale=float("inf")), "scale"),
     (dict(scale=float("nan")), "scale"), (dict(B=(1 << 24) - 1, m=65536, n=65536), "too large"),
+    (dict(B=(1 << 22) + 1, m=100, n=65), "too large"),
     (dict(coeffs=(4.0, 0.0, 0.0)), "bounded"), (dict(coeffs=(2.0, 0.0, 0.0)), "bounded"),
     (dict(coeffs=(1.0, float("nan"), 0.0)), "bounded"), (dict(coeffs=(1.0, -20.0, 20.0)), "bounded"),
     (dict(g=None), "g is NULL"), (dict(out=None), "out"), (dict(g=ODD), "aligned"),
