@@ -367,3 +367,24 @@ def test_more_rows_than_one_grid_holds(H, residual):
         assert torch.equal(r.y[lo:lo + 40], want.y) and torch.equal(r.rstd[lo:lo + 40], want.rstd)
         if residual:
             assert torch.equal(r.sum[lo:lo + 40], want.sum)
+
+
+def test_e4m3_scales_of_every_size():
+    """Blocks from 1e-43 to 1e37: the codes are those of the same rows at 1, where the scale is the same power of two larger;
+    NaN and infinities keep to their own codes and blocks."""
+    x = normal(32, 40, 128)
+    w = torch.ones(128, device="cuda")
+    base = m.moe_norm(x, w, kind="rms", out_dtype=torch.uint8)
+    for p in (-100, -90, -81, -79, -60, 60, 99, 101, 117):  # scales of about 2^-7: normal ones throughout
+        r = m.moe_norm(x, w * 2.0**p, kind="rms", out_dtype=torch.uint8)
+        assert torch.equal(r.y, base.y) and torch.equal(r.y_scales, base.y_scales * 2.0**p), p
+    for f in (1e-43, 1e-40):  # y itself and the scale are a few of fp32's smallest steps
+        r = m.moe_norm(x, w * f, kind="rms", out_dtype=torch.float8_e4m3fn)
+        assert torch.isfinite(r.y.float()).all() and (r.y_scales > 0).all()
+    w[7] = float("inf")
+    r = m.moe_norm(x, w, kind="rms", out_dtype=torch.float8_e4m3fn)
+    assert torch.isinf(r.y_scales).all() and torch.isnan(r.y[:, 7].float()).all()
+    assert (r.y.float()[:, 8:] == 0).all()
+    w[7] = float("nan")
+    r = m.moe_norm(x, w, kind="rms", out_dtype=torch.uint8)
+    assert (r.y[:, 7] & 0x7F == 0x7F).all() and (r.y[:, 8:] & 0x7F < 0x7F).all()
