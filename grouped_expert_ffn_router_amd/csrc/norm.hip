@@ -60,22 +60,23 @@ struct BwdArgs {
 };
 
 // 16 bytes of a row (VEC = 16 / ESZ elements), at the elements' own alignment: one wide access, which the memory system
-// splits where it crosses a line.  TAIL: H is no multiple of VEC, and a row's last elements go one by one (a variant of its
-// own: the code for them costs every width 20 to 50 registers, and with them resident wavefronts).
+// splits where it crosses a line.  TAIL: H is no multiple of VEC (a variant of its own: the code costs registers).  Then the
+// thread with a row's last few elements either loads them one by one (SINGLE), or loads the row's last 16 bytes, and
+// settle16 moves the elements to their places where they are used, zeros behind them.  bf16 rows take the second form, in
+// both directions (seven loads otherwise: forward 9717 x 1741 42.7 -> 34.6 us, backward 4252 x 10362 97 -> 72), fp32 rows
+// backward only, where loads run ahead of their use (32627 x 642 92 -> 77; forward 2000 x 15001 52 -> 53 or more), and
+// there without a condition on the load, which would wait for it (78 -> 133).  Rows of less than 16 bytes go one by one.
 typedef int i32x4_e4_t __attribute__((ext_vector_type(4), aligned(4)));
 typedef int i32x4_e2_t __attribute__((ext_vector_type(4), aligned(2)));
+typedef int i32x2_e2_t __attribute__((ext_vector_type(2), aligned(2)));
+typedef int i32_e2_t __attribute__((aligned(2)));
 
-template <int ESZ, bool TAIL>
-MOE_DEV i32x4_t load_row16(const uint8_t* row, int c, int H) {
+template <int ESZ, bool TAIL, bool SINGLE>
+MOE_DEV i32x4_t fetch_row16(const uint8_t* row, int c, int H) {
   constexpr int VEC = 16 / ESZ;
-  const uint8_t* p = row + (uint32_t)(c * ESZ);
   i32x4_t q = {0, 0, 0, 0};
-  if (c + VEC <= H) {
-    if constexpr (ESZ == 4)
-      q = *reinterpret_cast<const i32x4_e4_t*>(p);
-    else
-      q = *reinterpret_cast<const i32x4_e2_t*>(p);
-  } else if (TAIL && c < H) {
+  if (TAIL && (SINGLE ? c + VEC > H : H < VEC)) {
+    const uint8_t* p = row + (uint32_t)(c * ESZ);
 #pragma unroll
     for (int e = 0; e < VEC - 1; ++e)
       if (c + e < H) {
@@ -84,7 +85,32 @@ MOE_DEV i32x4_t load_row16(const uint8_t* row, int c, int H) {
         else
           q[e / 2] |= (int)((uint32_t)reinterpret_cast<const uint16_t*>(p)[e] << (16 * (e & 1)));
       }
+  } else if ((TAIL && ESZ == 4) || c < H) {
+    const uint8_t* p = row + (uint32_t)((TAIL && !SINGLE && c + VEC > H ? H - VEC : c) * ESZ);
+    if constexpr (ESZ == 4)
+      q = *reinterpret_cast<const i32x4_e4_t*>(p);
+    else
+      q = *reinterpret_cast<const i32x4_e2_t*>(p);
   }
+  return q;
+}
+template <int ESZ, bool TAIL, bool SINGLE>
+MOE_DEV void settle16(i32x4_t& q, int c, int H) {
+  constexpr int VEC = 16 / ESZ;
+  if (!TAIL || SINGLE || H < VEC || c + VEC <= H || (ESZ == 2 && c >= H)) return;
+  const int k = VEC - H % VEC;             // elements in front of this thread's own, the same in every thread
+  const int words = ESZ == 4 ? k : k / 2;  // 0 .. 3
+  if (words & 1) q = (i32x4_t){q[1], q[2], q[3], 0};
+  if (words & 2) q = (i32x4_t){q[2], q[3], 0, 0};
+  if (ESZ == 2 && (k & 1))
+#pragma unroll
+    for (int d = 0; d < 4; ++d) q[d] = (int)__builtin_amdgcn_alignbit(d < 3 ? (uint32_t)q[d + 1] : 0u, (uint32_t)q[d], 16);
+  if (ESZ == 4 && c >= H) q = (i32x4_t){0, 0, 0, 0};
+}
+template <int ESZ, bool TAIL>
+MOE_DEV i32x4_t load_row16(const uint8_t* row, int c, int H) {
+  i32x4_t q = fetch_row16<ESZ, TAIL, ESZ == 4>(row, c, H);
+  settle16<ESZ, TAIL, ESZ == 4>(q, c, H);
   return q;
 }
 template <int ESZ>
@@ -95,29 +121,34 @@ MOE_DEV float element(const i32x4_t& q, int e) {
 }
 template <int ESZ, bool TAIL, int VEC>
 MOE_DEV void store_row16(uint8_t* row, int c, int H, const float (&v)[VEC]) {
+  if (c >= H) return;
   uint8_t* p = row + (uint32_t)(c * ESZ);
-  if (c + VEC <= H) {
-    i32x4_t q;
+  i32x4_t q;
 #pragma unroll
-    for (int d = 0; d < 4; ++d) {
-      if constexpr (ESZ == 4)
-        q[d] = __float_as_int(v[d]);
-      else
-        q[d] = (int)((uint32_t)f32_to_bf16_bits(v[2 * d]) | ((uint32_t)f32_to_bf16_bits(v[2 * d + 1]) << 16));
-    }
+  for (int d = 0; d < 4; ++d) {
+    if constexpr (ESZ == 4)
+      q[d] = __float_as_int(v[d]);
+    else
+      q[d] = (int)((uint32_t)f32_to_bf16_bits(v[2 * d]) | ((uint32_t)f32_to_bf16_bits(v[2 * d + 1]) << 16));
+  }
+  if (!TAIL || c + VEC <= H) {
     if constexpr (ESZ == 4)
       *reinterpret_cast<i32x4_e4_t*>(p) = q;
     else
       *reinterpret_cast<i32x4_e2_t*>(p) = q;
-  } else if (TAIL && c < H) {
+    return;
+  }
+  if constexpr (ESZ == 4) {
 #pragma unroll
     for (int e = 0; e < VEC - 1; ++e)
-      if (c + e < H) {
-        if constexpr (ESZ == 4)
-          reinterpret_cast<float*>(p)[e] = v[e];
-        else
-          reinterpret_cast<uint16_t*>(p)[e] = f32_to_bf16_bits(v[e]);
-      }
+      if (c + e < H) reinterpret_cast<float*>(p)[e] = v[e];
+  } else {  // the last H % VEC elements as 8, 4 and 2 bytes
+    const int words = H % VEC / 2;
+    if (words & 2) *reinterpret_cast<i32x2_e2_t*>(p) = (i32x2_t){q[0], q[1]};
+    if (words & 1) *reinterpret_cast<i32_e2_t*>(p + (words & 2) * 4) = words & 2 ? q[2] : q[0];
+    if (H & 1)
+      *reinterpret_cast<uint16_t*>(p + words * 4) =
+          (uint16_t)(words == 0 ? q[0] : words == 1 ? q[1] : words == 2 ? q[2] : q[3]);
   }
 }
 // VEC columns of the weight or bias: fp32 or bf16 by a launch-uniform flag; 0 past H
@@ -188,14 +219,16 @@ __global__ __launch_bounds__((TPR < 256 ? 256 : TPR)) void norm_fwd_kernel(const
   const int64_t rr = live ? row : a.T - 1;  // surplus threads compute the last row and store nothing
   i32x4_t raw[NV];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) raw[i] = load_row16<ESZ, TAIL>(a.x + rr * a.ldx * ESZ, (i * TPR + t) * VEC, a.H);
+  for (int i = 0; i < NV; ++i) raw[i] = fetch_row16<ESZ, TAIL, ESZ == 4>(a.x + rr * a.ldx * ESZ, (i * TPR + t) * VEC, a.H);
   float v[NV][VEC];
   if (a.res != nullptr) {
     i32x4_t res[NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) res[i] = load_row16<ESZ, TAIL>(a.res + rr * a.ldr * ESZ, (i * TPR + t) * VEC, a.H);
+    for (int i = 0; i < NV; ++i) res[i] = fetch_row16<ESZ, TAIL, ESZ == 4>(a.res + rr * a.ldr * ESZ, (i * TPR + t) * VEC, a.H);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
+      settle16<ESZ, TAIL, ESZ == 4>(raw[i], (i * TPR + t) * VEC, a.H);
+      settle16<ESZ, TAIL, ESZ == 4>(res[i], (i * TPR + t) * VEC, a.H);
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
         v[i][e] = element<ESZ>(raw[i], e) + element<ESZ>(res[i], e);
@@ -205,9 +238,11 @@ __global__ __launch_bounds__((TPR < 256 ? 256 : TPR)) void norm_fwd_kernel(const
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+    for (int i = 0; i < NV; ++i) {
+      settle16<ESZ, TAIL, ESZ == 4>(raw[i], (i * TPR + t) * VEC, a.H);
 #pragma unroll
       for (int e = 0; e < VEC; ++e) v[i][e] = element<ESZ>(raw[i], e);
+    }
   }
   const float h = (float)a.H;
   float m = 0.0f;
@@ -328,8 +363,8 @@ __global__ __launch_bounds__((TPR < 256 ? 256 : TPR)) void norm_bwd_kernel(const
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (i * TPR + t) * VEC;
-      qy[i] = load_row16<ESZ, TAIL>(a.dy + row * a.ld_dy * ESZ, c, a.H);
-      qs[i] = load_row16<ESZ, TAIL>(a.s + row * a.ld_s * ESZ, c, a.H);
+      qy[i] = fetch_row16<ESZ, TAIL, false>(a.dy + row * a.ld_dy * ESZ, c, a.H);
+      qs[i] = fetch_row16<ESZ, TAIL, false>(a.s + row * a.ld_s * ESZ, c, a.H);
     }
     if (!a.rms) m = a.mean[row];
     r = a.rstd[row];
@@ -343,7 +378,9 @@ __global__ __launch_bounds__((TPR < 256 ? 256 : TPR)) void norm_bwd_kernel(const
     const float rs = r;
     float c12[2] = {0.0f, 0.0f};
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+    for (int i = 0; i < NV; ++i) {
+      settle16<ESZ, TAIL, false>(qy[i], (i * TPR + t) * VEC, a.H);
+      settle16<ESZ, TAIL, false>(qs[i], (i * TPR + t) * VEC, a.H);
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
         const bool in = (i * TPR + t) * VEC + (TAIL ? e : 0) < a.H && live;
@@ -355,11 +392,12 @@ __global__ __launch_bounds__((TPR < 256 ? 256 : TPR)) void norm_bwd_kernel(const
         c12[0] += tw[i][e];
         c12[1] = __builtin_fmaf(tw[i][e], z[i][e], c12[1]);
       }
+    }
     i32x4_t qd[NV];
     if (a.dsum != nullptr) {
       const int64_t rr = live ? row : a.T - 1;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) qd[i] = load_row16<ESZ, TAIL>(a.dsum + rr * a.ld_dsum * ESZ, (i * TPR + t) * VEC, a.H);
+      for (int i = 0; i < NV; ++i) qd[i] = fetch_row16<ESZ, TAIL, false>(a.dsum + rr * a.ld_dsum * ESZ, (i * TPR + t) * VEC, a.H);
     }
     if (r0 + step < a.T) fetch(r0 + step);
     row_sum<TPR, THREADS, 2>(c12, red, flip);
@@ -370,9 +408,11 @@ __global__ __launch_bounds__((TPR < 256 ? 256 : TPR)) void norm_bwd_kernel(const
         float d[VEC];
 #pragma unroll
         for (int e = 0; e < VEC; ++e) d[e] = (tw[i][e] - c1 - z[i][e] * c2) * rs;
-        if (a.dsum != nullptr)
+        if (a.dsum != nullptr) {
+          settle16<ESZ, TAIL, false>(qd[i], (i * TPR + t) * VEC, a.H);
 #pragma unroll
           for (int e = 0; e < VEC; ++e) d[e] += element<ESZ>(qd[i], e);
+        }
         store_row16<ESZ, TAIL, VEC>(a.dx + row * a.H * ESZ, (i * TPR + t) * VEC, a.H, d);
       }
   }

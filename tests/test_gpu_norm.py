@@ -388,3 +388,22 @@ def test_e4m3_scales_of_every_size():
     w[7] = float("nan")
     r = m.moe_norm(x, w, kind="rms", out_dtype=torch.uint8)
     assert (r.y[:, 7] & 0x7F == 0x7F).all() and (r.y[:, 8:] & 0x7F < 0x7F).all()
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("base", [0, 16, 640, 2048])
+def test_every_rest_of_a_row(base, dt):
+    """Widths of each remainder by 8, rows that end where NaN begins: none of it is read into a row, and none is overwritten."""
+    for H in range(base + 1, base + 10):
+        T = 9
+        wide = [torch.full((T, H + 3), float("nan"), device="cuda", dtype=dt) for _ in range(4)]
+        x, res, dy, ds = (t[:, 1:H + 1] for t in wide)
+        for k, t in enumerate((x, res, dy, ds)):
+            t.copy_(normal(50 + k, T, H))
+        w, b = normal(54, H).to(dt), normal(55, H).to(dt)
+        f = m.moe_norm(x, w, b, res, "layer", 1e-5)
+        check_forward(f, x, w, b, res, "layer", 1e-5)
+        for kind, g in (("layer", f), ("rms", m.moe_norm(x, w, None, res, "rms", 1e-5))):
+            out = m.moe_norm_backward(dy, g.sum, w, g.mean, g.rstd, kind, ds, want_bias=True)
+            check_backward(out, dy, g.sum, w, g.mean, g.rstd, kind, ds)
+        assert all(torch.isnan(t[:, 0]).all() and torch.isnan(t[:, H + 1:]).all() for t in wide)
