@@ -9,7 +9,8 @@ terms added in any order is off by at most n u32 sum|terms|; a row's sums have a
   y:      |w| r d + |z w| (rel(rstd) + 4 u32) + 2 u32 |y - b| + 2 u32 |b| + u |y|
   dx:     r N u32 (|t| + mean|t| + |z| mean|t z|) + u32 |dsum| + u |dx|, t = dy w
   dw, db: sums over rows: a workgroup adds at most T / 256 + 1 rows (256 workgroups or more, or one pass), 16 groups, and
-          the partials in 32 + 32: (T / 256 + 112) u32 sum|dy z|
+          the partials in 32 + 32: (T / 256 + 112) u32 sum|dy z|.  Wide rows have 64 workgroups or more a column and no
+          groups, T / 64 + 1 + 64 terms: less than that up to T = 4000
 """
 import math
 
